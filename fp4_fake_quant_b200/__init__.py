@@ -10,7 +10,10 @@ from .binding import (QF_MXFP4, QF_NVFP4, QF_Q4K, QF_X_BF16, QF_X_F32, FORMATS, 
                       qf_amax_fakequant_lora, qf_amax_fakequant_noalloc, qf_amax_tied, qf_amax_tied_lora, qf_fakequant,
                       qf_fakequant_lora, qf_lora_merge, qf_pack, qf_ste_backward,
                       qf_noalloc_check, qf_test_barrier_timeout, qf_workspace_check,
-                      workspace_bytes, lib)
+                      workspace_bytes, lib,
+                      QF_STATE_BLOCK, QF_STATE_E4M3, QF_STATE_F32, PreparedStep, alloc_adamw_state,
+                      alloc_grad_norm_workspace, prepare_adamw, prepare_grad_norm, qf_adamw,
+                      qf_grad_norm)
 
 __all__ = ["QF_NVFP4", "QF_MXFP4", "QF_Q4K", "QF_X_BF16", "QF_X_F32", "FORMATS", "EXPORTS",
            "QfError", "alloc_outputs", "alloc_workspace", "output_sizes",
@@ -19,4 +22,7 @@ __all__ = ["QF_NVFP4", "QF_MXFP4", "QF_Q4K", "QF_X_BF16", "QF_X_F32", "FORMATS",
            "qf_amax_fakequant_lora", "qf_amax_fakequant_noalloc", "qf_amax_tied", "qf_amax_tied_lora", "qf_fakequant",
            "qf_fakequant_lora", "qf_lora_merge", "qf_pack", "qf_ste_backward",
            "qf_noalloc_check", "qf_test_barrier_timeout", "qf_workspace_check",
-           "workspace_bytes", "lib"]
+           "workspace_bytes", "lib",
+           "QF_STATE_BLOCK", "QF_STATE_E4M3", "QF_STATE_F32", "PreparedStep", "alloc_adamw_state",
+           "alloc_grad_norm_workspace", "prepare_adamw", "prepare_grad_norm", "qf_adamw",
+           "qf_grad_norm"]

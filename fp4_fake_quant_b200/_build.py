@@ -9,7 +9,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqf.so")
-SOURCES = ["qf_api.cu"]
+SOURCES = ["qf_api.cu", "qf_adamw.cu"]
 HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith(".cuh"))   # every header counts
 
 NVCC_FLAGS = [
@@ -17,7 +17,7 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     "-fmad=false",                 # no FMA contraction: the rounding order is part of the ABI
     "-Xcompiler", "-fPIC", "-shared",
-    "-Xptxas", "-v",
+    "-Xptxas", "-v", "--threads", "4",
 ]
 
 

@@ -38,6 +38,23 @@ class QfLora(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class QfParam(ctypes.Structure):
+    """Mirror of ``qf_param`` (include/qf.h)."""
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("w", ctypes.c_void_p), ("numel", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+                ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class QfAdamwOpt(ctypes.Structure):
+    """Mirror of ``qf_adamw_opt`` (include/qf.h)."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("d_lr", ctypes.c_void_p),
+                ("d_step", ctypes.c_void_p), ("d_grad_scale", ctypes.c_void_p),
+                ("p_type", ctypes.c_int32), ("g_type", ctypes.c_int32), ("state", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class QfError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -68,7 +85,13 @@ def _load() -> ctypes.CDLL:
     lib.qf_noalloc_check.argtypes = [P]
     lib.qf_test_barrier_timeout.argtypes = [ctypes.c_uint]
     lib.qf_test_barrier_timeout.restype = None
-    for f in (lib.qf_amax_tied, lib.qf_fakequant, lib.qf_pack, lib.qf_ste_backward,
+    O = ctypes.POINTER(QfAdamwOpt)
+    Q = ctypes.POINTER(QfParam)
+    lib.qf_adamw.argtypes = [Q, I, O, P, I, P]
+    lib.qf_grad_norm.argtypes = [Q, I, I, ctypes.c_double, P, P, P, ctypes.c_size_t, P]
+    lib.qf_grad_norm_workspace_bytes.argtypes = []
+    lib.qf_grad_norm_workspace_bytes.restype = ctypes.c_size_t
+    for f in (lib.qf_adamw, lib.qf_grad_norm, lib.qf_amax_tied, lib.qf_fakequant, lib.qf_pack, lib.qf_ste_backward,
               lib.qf_lora_merge, lib.qf_amax_tied_lora, lib.qf_fakequant_lora,
               lib.qf_amax_fakequant, lib.qf_workspace_check, lib.qf_amax_fakequant_noalloc,
               lib.qf_amax_fakequant_lora, lib.qf_noalloc_check):
@@ -89,6 +112,7 @@ EXPORTS = ("qf_amax_tied", "qf_fakequant", "qf_pack", "qf_ste_backward", "qf_lor
            "qf_amax_tied_lora", "qf_fakequant_lora", "qf_amax_fakequant_lora",
            "qf_amax_fakequant", "qf_amax_fakequant_workspace_bytes", "qf_workspace_check",
            "qf_amax_fakequant_noalloc", "qf_noalloc_check", "qf_test_barrier_timeout",
+           "qf_adamw", "qf_grad_norm", "qf_grad_norm_workspace_bytes",
            "qf_status_string", "qf_last_error", "qf_version")
 
 
@@ -354,3 +378,173 @@ def prepare_amax_tied_lora(xs, adapters, groups, group_amax) -> "Prepared":
     la = _lora(adapters)
     keep = (arr, la, list(xs), list(adapters), group_amax)
     return Prepared(lib.qf_amax_tied_lora, (arr, la, n, _ptr(group_amax), group_amax.numel()), keep)
+
+
+X_TYPES = {torch.bfloat16: QF_X_BF16, torch.float32: QF_X_F32}
+QF_STATE_F32, QF_STATE_E4M3, QF_STATE_BLOCK = 0, 1, 256
+
+
+def _on_device(what: str, ts, device=None) -> torch.device:
+    """Every tensor of ``ts`` (None entries aside) lies on one CUDA device, the current one."""
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: tensors passed to libqf must be CUDA tensors")
+        if device is None:
+            device = t.device
+            if device.index != torch.cuda.current_device():
+                raise ValueError(f"{what}: tensors lie on {device}, the current device is "
+                                 f"cuda:{torch.cuda.current_device()}")
+        elif t.device != device:
+            raise ValueError(f"{what}: tensors on {device} and {t.device} in one call")
+    return device
+
+
+def _one_type(what: str, ts, allowed):
+    kinds = {t.dtype for t in ts}
+    if len(kinds) > 1:
+        raise TypeError(f"{what}: one call takes tensors of one type, got {sorted(map(str, kinds))}")
+    kind = kinds.pop() if kinds else next(iter(allowed))
+    if kind not in allowed:
+        raise TypeError(f"{what} must be {' or '.join(str(a)[6:] for a in allowed)}, got {kind}")
+    return kind
+
+
+def _scalar(what: str, t, dtype):
+    if t is not None and (t.dtype != dtype or t.numel() != 1):
+        raise TypeError(f"{what} must be one {str(dtype)[6:]} value on the device")
+    return _ptr(t)
+
+
+def alloc_adamw_state(p: torch.Tensor, bits: int = 32):
+    """Zeroed states (m, v, m_scale, v_scale) of one parameter tensor (a torch allocation):
+    FP32 moments and no scales, or E4M3 bytes with an FP32 scale per 256 elements."""
+    if bits == 32:
+        return (torch.zeros(p.shape, dtype=torch.float32, device=p.device),
+                torch.zeros(p.shape, dtype=torch.float32, device=p.device), None, None)
+    if bits != 8:
+        raise ValueError("bits must be 8 or 32")
+    blocks = (p.numel() + QF_STATE_BLOCK - 1) // QF_STATE_BLOCK
+    return (torch.zeros(p.shape, dtype=torch.uint8, device=p.device),
+            torch.zeros(p.shape, dtype=torch.uint8, device=p.device),
+            torch.zeros(blocks, device=p.device), torch.zeros(blocks, device=p.device))
+
+
+def _adamw_args(params, grads, ms, vs, lr, betas, eps, weight_decay, m_scales, v_scales, copies,
+                groups, group_amax, lr_tensor, step_tensor, grad_scale):
+    n = len(params)
+    for name, ts in (("grads", grads), ("ms", ms), ("vs", vs), ("m_scales", m_scales),
+                     ("v_scales", v_scales), ("copies", copies), ("groups", groups)):
+        if ts is not None and len(ts) != n:
+            raise ValueError(f"{name}: {len(ts)} for {n} parameters")
+    pt, gt = _one_type("params", params, X_TYPES), _one_type("grads", grads, X_TYPES)
+    st = _one_type("ms and vs", [*ms, *vs], {torch.float32: QF_STATE_F32, torch.uint8: QF_STATE_E4M3})
+    e4m3 = st == torch.uint8
+    if e4m3 and (m_scales is None or v_scales is None):
+        raise ValueError("8-bit states need m_scales and v_scales")
+    _on_device("qf_adamw", [*params, *grads, *ms, *vs, *((*m_scales, *v_scales) if e4m3 else ()),
+                            *(copies or ()), group_amax, lr_tensor, step_tensor, grad_scale])
+    if group_amax is not None and (group_amax.dtype != torch.float32 or groups is None):
+        raise TypeError("group_amax must be float32 and comes with groups")
+    decay = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+    if len(decay) != n:
+        raise ValueError(f"weight_decay: {len(decay)} for {n} parameters")
+    arr = (QfParam * max(n, 1))()
+    for i in range(n):
+        d, size = arr[i], params[i].numel()
+        for what, t in (("grads", grads[i]), ("ms", ms[i]), ("vs", vs[i]),
+                        ("copies", copies[i] if copies is not None else None)):
+            if t is not None and t.numel() != size:
+                raise ValueError(f"{what}[{i}]: {t.numel()} elements for {size} parameters")
+        d.p, d.g, d.m, d.v = _ptr(params[i]), _ptr(grads[i]), _ptr(ms[i]), _ptr(vs[i])
+        if e4m3:
+            blocks = (size + QF_STATE_BLOCK - 1) // QF_STATE_BLOCK
+            for what, t in (("m_scales", m_scales[i]), ("v_scales", v_scales[i])):
+                if t.dtype != torch.float32 or t.numel() != blocks:
+                    raise ValueError(f"{what}[{i}] must hold {blocks} float32 values")
+            d.m_scale, d.v_scale = _ptr(m_scales[i]), _ptr(v_scales[i])
+        if copies is not None and copies[i] is not None:
+            if copies[i].dtype != torch.bfloat16:
+                raise TypeError("copies must be bfloat16")
+            d.w = _ptr(copies[i])
+        d.numel, d.weight_decay = size, float(decay[i])
+        d.group = -1 if groups is None or groups[i] is None else int(groups[i])
+    opt = QfAdamwOpt(lr=float(lr), beta1=float(betas[0]), beta2=float(betas[1]), eps=float(eps), step=1,
+                     d_lr=_scalar("lr_tensor", lr_tensor, torch.float32),
+                     d_step=_scalar("step_tensor", step_tensor, torch.int64),
+                     d_grad_scale=_scalar("grad_scale", grad_scale, torch.float32),
+                     p_type=X_TYPES[pt], g_type=X_TYPES[gt],
+                     state=QF_STATE_E4M3 if e4m3 else QF_STATE_F32)
+    ng = group_amax.numel() if group_amax is not None else 0
+    keep = (params, grads, ms, vs, m_scales, v_scales, copies, group_amax, lr_tensor, step_tensor,
+            grad_scale)
+    return arr, n, opt, _ptr(group_amax), ng, keep
+
+
+class PreparedStep:
+    """qf_adamw marshalled once: calling it with a step number (and, if it changed, a
+    learning rate) enqueues that step."""
+
+    def __init__(self, arr, n, opt, amax, ng, keep):
+        self.opt = opt
+        self._args = (arr, n, ctypes.byref(opt), amax, ng)
+        self._keep = (keep, arr)
+
+    def __call__(self, step: int = 1, lr: Optional[float] = None, stream=None) -> None:
+        self.opt.step = step
+        if lr is not None:
+            self.opt.lr = lr
+        _check(lib.qf_adamw(*self._args, _stream(stream)))
+
+
+def prepare_adamw(params, grads, ms, vs, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+                  m_scales=None, v_scales=None, copies=None, groups=None, group_amax=None,
+                  lr_tensor=None, step_tensor=None, grad_scale=None) -> PreparedStep:
+    return PreparedStep(*_adamw_args(params, grads, ms, vs, lr, betas, eps, weight_decay, m_scales,
+                                     v_scales, copies, groups, group_amax, lr_tensor, step_tensor,
+                                     grad_scale))
+
+
+def qf_adamw(params, grads, ms, vs, lr, step=1, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
+             m_scales=None, v_scales=None, copies=None, groups=None, group_amax=None, lr_tensor=None,
+             step_tensor=None, grad_scale=None, stream=None) -> None:
+    """One AdamW step of many tensors, in place.  ``ms``/``vs`` float32: the moments; uint8:
+    E4M3 codes of m and of sqrt(v) behind ``m_scales``/``v_scales`` (``alloc_adamw_state``).
+    ``weight_decay``: one value, or one per tensor.  ``group_amax`` receives the tie groups'
+    max |p| of the updated weights (``groups[i]`` None: in no group).  ``lr_tensor``,
+    ``step_tensor``, ``grad_scale``: device scalars read when the step runs."""
+    prepare_adamw(params, grads, ms, vs, lr, betas, eps, weight_decay, m_scales, v_scales, copies,
+                  groups, group_amax, lr_tensor, step_tensor, grad_scale)(step, stream=stream)
+
+
+def alloc_grad_norm_workspace(device=None) -> torch.Tensor:
+    """A zeroed qf_grad_norm workspace (a torch allocation; plumbing)."""
+    return torch.zeros(int(lib.qf_grad_norm_workspace_bytes()), dtype=torch.uint8,
+                       device=torch.device(device) if device is not None else torch.device("cuda"))
+
+
+def prepare_grad_norm(grads, norm, max_norm=0.0, step_tensor=None, workspace=None) -> Prepared:
+    gt = _one_type("grads", grads, X_TYPES)
+    if norm.dtype != torch.float32 or norm.numel() != 2:
+        raise TypeError("norm must be two float32 values on the device")
+    if workspace is None:
+        workspace = alloc_grad_norm_workspace(norm.device)
+    _on_device("qf_grad_norm", [norm, *grads, step_tensor, workspace])
+    arr = (QfParam * max(len(grads), 1))()
+    for d, g in zip(arr, grads):
+        d.g, d.numel = _ptr(g), g.numel()
+    return Prepared(lib.qf_grad_norm,
+                    (arr, len(grads), X_TYPES[gt], float(max_norm), _ptr(norm),
+                     _scalar("step_tensor", step_tensor, torch.int64), _ptr(workspace),
+                     workspace.numel() * workspace.element_size()),
+                    (arr, list(grads), norm, step_tensor, workspace))
+
+
+def qf_grad_norm(grads, norm, max_norm=0.0, step_tensor=None, workspace=None, stream=None):
+    """norm <- (global L2 norm of the gradients, the scale that clips it to max_norm); the
+    scale is NaN, which makes qf_adamw skip its step, when a gradient is not finite.
+    ``step_tensor`` (int64) is advanced by one otherwise.  Without a ``workspace`` one is
+    allocated for the call."""
+    prepare_grad_norm(grads, norm, max_norm, step_tensor, workspace)(stream)
+    return norm

@@ -1,0 +1,251 @@
+// qf_adamw.cu -- the optimizer-step entry points of libqf.so: qf_adamw and qf_grad_norm
+// (declared in include/qf.h).  Host-side argument validation, descriptor tables, launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "qf.h"
+#include "qf_adamw.cuh"
+#include "qf_host.cuh"
+
+namespace {
+
+using namespace qf_host;
+using qf::AdamScalars;
+using qf::DevParam;
+using qf::NormTable;
+using qf::NormTask;
+using qf::ParamTable;
+using qf::kAdamThreads;
+using qf::kLargeP;
+using qf::kParamBlock;
+using qf::kSmallP;
+
+#ifndef QF_ADAM_WAVES
+#define QF_ADAM_WAVES 1         // grid: CTAs per resident slot (1 = persistent)
+#endif
+
+int size_of(int type) { return type == QF_X_F32 ? 4 : 2; }
+int64_t units_of(int64_t numel) { return (numel + kParamBlock - 1) / kParamBlock; }
+
+qf_status check_param(const qf_param& t, int i, const qf_adamw_opt& o, const float* amax,
+                      int n_groups) {
+    if (t.numel < 0) return fail(QF_ERR_SHAPE, "tensor %d: numel = %lld < 0", i, (long long)t.numel);
+    if (t.numel > INT64_MAX / 8) return fail(QF_ERR_SHAPE, "tensor %d: numel overflows", i);
+    if (amax && (t.group < -1 || t.group >= n_groups))
+        return fail(QF_ERR_INVALID_ARG, "tensor %d: group %d outside [-1, %d)", i, t.group, n_groups);
+    if (!(t.weight_decay >= 0.0) || std::isinf(t.weight_decay))
+        return fail(QF_ERR_INVALID_ARG, "tensor %d: weight_decay is not a finite value >= 0", i);
+    if (t.numel == 0) return QF_OK;
+    const bool s8 = o.state == QF_STATE_E4M3;
+    if (!t.p || !t.g || !t.m || !t.v) return fail(QF_ERR_INVALID_ARG, "tensor %d: p, g, m or v is NULL", i);
+    if (s8 && (!t.m_scale || !t.v_scale))
+        return fail(QF_ERR_INVALID_ARG, "tensor %d: 8-bit states need m_scale and v_scale", i);
+    if (t.w && o.p_type != QF_X_F32)
+        return fail(QF_ERR_INVALID_ARG, "tensor %d: a BF16 copy needs FP32 parameters", i);
+    if (!aligned16(t.p) || !aligned16(t.g) || !aligned16(t.m) || !aligned16(t.v) || !aligned16(t.w))
+        return fail(QF_ERR_ALIGN, "tensor %d: p, g, m, v or w not 16-byte aligned", i);
+    if (s8 && ((reinterpret_cast<uintptr_t>(t.m_scale) | reinterpret_cast<uintptr_t>(t.v_scale)) & 3))
+        return fail(QF_ERR_ALIGN, "tensor %d: m_scale or v_scale not 4-byte aligned", i);
+    const int64_t ns = s8 ? t.numel : 4 * t.numel, nsc = s8 ? 4 * units_of(t.numel) : 0;
+    const void* const ptr[7] = {t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.w};
+    const int64_t len[7] = {t.numel * size_of(o.p_type), t.numel * size_of(o.g_type), ns, ns, nsc, nsc,
+                            2 * t.numel};
+    for (int a = 0; a < 7; ++a)
+        for (int b = a + 1; b < 7; ++b)
+            if (overlap(ptr[a], len[a], ptr[b], len[b]))
+                return fail(QF_ERR_INVALID_ARG, "tensor %d: p, g, the states and w must not overlap", i);
+    return QF_OK;
+}
+
+template <typename PT, typename GT, bool S8, int MAXT>
+qf_status adam_launch(const qf_param* t, int n, const AdamScalars& h, float* amax, cudaStream_t s) {
+    ParamTable<MAXT> P;                         // at most 31 KB
+    Shape L;
+    qf_status st = shape_of(qf::k_adamw<PT, GT, S8, MAXT>, kAdamThreads, 0, &L);
+    if (st != QF_OK) return st;
+    int k = 0;
+    int64_t units = 0;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].numel == 0) continue;
+        DevParam& d = P.t[k++];
+        d.p = t[i].p;
+        d.g = t[i].g;
+        d.m = t[i].m;
+        d.v = t[i].v;
+        d.ms = t[i].m_scale;
+        d.vs = t[i].v_scale;
+        d.w = static_cast<uint16_t*>(t[i].w);
+        d.wd = t[i].weight_decay;
+        d.numel = t[i].numel;
+        d.unit_begin = units;
+        d.group = amax ? t[i].group : -1;
+        d.pad = 0;
+        units += units_of(t[i].numel);
+    }
+    P.h = h;
+    P.n = k;
+    P.total_units = units;
+    P.amax = reinterpret_cast<uint32_t*>(amax);
+    const int64_t want = (units + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
+    const int64_t cap = (int64_t)L.sms * L.per_sm * QF_ADAM_WAVES;
+    qf::k_adamw<PT, GT, S8, MAXT><<<(unsigned)std::min(want, cap), kAdamThreads, 0, s>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? QF_OK : cuda_fail(e, "kernel launch");
+}
+
+// The tensors in launches of at most kLargeP (empty ones are dropped).
+template <typename PT, typename GT, bool S8>
+qf_status adam_all(const qf_param* t, int n, const AdamScalars& h, float* amax, cudaStream_t s) {
+    for (int at = 0; at < n;) {
+        int end = at, live = 0;
+        while (end < n && live + (t[end].numel > 0) <= kLargeP) live += t[end++].numel > 0;
+        qf_status st = QF_OK;
+        if (live > kSmallP) st = adam_launch<PT, GT, S8, kLargeP>(t + at, end - at, h, amax, s);
+        else if (live > 0) st = adam_launch<PT, GT, S8, kSmallP>(t + at, end - at, h, amax, s);
+        if (st != QF_OK) return st;
+        at = end;
+    }
+    return QF_OK;
+}
+
+template <typename PT, typename GT>
+qf_status adam_states(const qf_param* t, int n, int state, const AdamScalars& h, float* amax,
+                      cudaStream_t s) {
+    return state == QF_STATE_E4M3 ? adam_all<PT, GT, true>(t, n, h, amax, s)
+                                  : adam_all<PT, GT, false>(t, n, h, amax, s);
+}
+
+constexpr int kSmallN = 16, kLargeN = 1024;       // 24-byte entries: 24 KB of kernel parameters
+
+template <typename GT, int MAXT>
+qf_status norm_launch(const qf_param* t, int n, double max_norm, float* out, int64_t* d_step,
+                      qf::NormState* ws, bool first, bool last, cudaStream_t s) {
+    constexpr int64_t kUnit = 32 * (16 / sizeof(GT)) * qf::kNormVecs;
+    NormTable<MAXT> P;
+    Shape L;
+    qf_status st = shape_of(qf::k_grad_norm<GT, MAXT>, kAdamThreads, 0, &L);
+    if (st != QF_OK) return st;
+    int k = 0;
+    int64_t units = 0;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].numel == 0) continue;
+        P.t[k++] = NormTask{t[i].g, t[i].numel, units};
+        units += (t[i].numel + kUnit - 1) / kUnit;
+    }
+    P.ws = ws;
+    P.out = out;
+    P.d_step = d_step;
+    P.max_norm = max_norm;
+    P.total_units = units;
+    P.n = k;
+    P.first = first;
+    P.last = last;
+    const int64_t want = std::max<int64_t>(1, (units + kAdamThreads / 32 - 1) / (kAdamThreads / 32));
+    const int64_t cap = std::min<int64_t>((int64_t)L.sms * L.per_sm, qf::kNormMaxGrid);
+    qf::k_grad_norm<GT, MAXT><<<(unsigned)std::min(want, cap), kAdamThreads, 0, s>>>(P);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? QF_OK : cuda_fail(e, "kernel launch");
+}
+
+template <typename GT>
+qf_status norm_all(const qf_param* t, int n, double max_norm, float* out, int64_t* d_step,
+                   qf::NormState* ws, cudaStream_t s) {
+    int at = 0;
+    do {
+        int end = at, live = 0;
+        while (end < n && live + (t[end].numel > 0) <= kLargeN) live += t[end++].numel > 0;
+        const qf_status st =
+            live > kSmallN
+                ? norm_launch<GT, kLargeN>(t + at, end - at, max_norm, out, d_step, ws, at == 0, end == n, s)
+                : norm_launch<GT, kSmallN>(t + at, end - at, max_norm, out, d_step, ws, at == 0, end == n, s);
+        if (st != QF_OK) return st;
+        at = end;
+    } while (at < n);
+    return QF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qf_status qf_adamw(const qf_param* t, int n, const qf_adamw_opt* opt, float* d_group_amax,
+                   int n_groups, void* stream) {
+    g_err[0] = 0;
+    if (opt == nullptr) return fail(QF_ERR_INVALID_ARG, "opt is NULL");
+    const qf_adamw_opt& o = *opt;
+    if (n < 0) return fail(QF_ERR_INVALID_ARG, "n = %d < 0", n);
+    if (n > 0 && t == nullptr) return fail(QF_ERR_INVALID_ARG, "tensor array is NULL");
+    for (int type : {o.p_type, o.g_type})
+        if (type != QF_X_BF16 && type != QF_X_F32)
+            return fail(QF_ERR_UNSUPPORTED, "unknown parameter or gradient type %d", type);
+    if (o.state != QF_STATE_F32 && o.state != QF_STATE_E4M3)
+        return fail(QF_ERR_UNSUPPORTED, "unknown state type %d", (int)o.state);
+    if (!(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0))
+        return fail(QF_ERR_INVALID_ARG, "beta1 and beta2 must lie in [0, 1)");
+    if (!(o.eps >= 0.0) || std::isinf(o.eps)) return fail(QF_ERR_INVALID_ARG, "eps is not a finite value >= 0");
+    if (!o.d_lr && !std::isfinite(o.lr)) return fail(QF_ERR_INVALID_ARG, "lr is not finite");
+    if (!o.d_step && o.step < 1) return fail(QF_ERR_INVALID_ARG, "step = %lld < 1", (long long)o.step);
+    if (d_group_amax && n_groups <= 0) return fail(QF_ERR_INVALID_ARG, "n_groups = %d <= 0", n_groups);
+    for (int i = 0; i < n; ++i) {
+        const qf_status st = check_param(t[i], i, o, d_group_amax, n_groups);
+        if (st != QF_OK) return st;
+    }
+    AdamScalars h{};
+    h.lr = o.lr;
+    h.beta1 = o.beta1;
+    h.beta2 = o.beta2;
+    h.b1 = (float)o.beta1;
+    h.omb1 = (float)(1.0 - o.beta1);
+    h.b2 = (float)o.beta2;
+    h.omb2 = (float)(1.0 - o.beta2);
+    h.eps = (float)o.eps;
+    h.d_lr = o.d_lr;
+    h.d_step = o.d_step;
+    h.d_grad_scale = o.d_grad_scale;
+    h.step = o.step;
+    if (!o.d_lr && !o.d_step) qf::adam_step_scalars(o.lr, o.beta1, o.beta2, o.step, &h.ss, &h.rs2);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (d_group_amax) {
+        const cudaError_t e = cudaMemsetAsync(d_group_amax, 0, sizeof(float) * n_groups, s);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (o.p_type == QF_X_F32)
+        return o.g_type == QF_X_F32 ? adam_states<float, float>(t, n, o.state, h, d_group_amax, s)
+                                    : adam_states<float, uint16_t>(t, n, o.state, h, d_group_amax, s);
+    return o.g_type == QF_X_F32 ? adam_states<uint16_t, float>(t, n, o.state, h, d_group_amax, s)
+                                : adam_states<uint16_t, uint16_t>(t, n, o.state, h, d_group_amax, s);
+}
+
+size_t qf_grad_norm_workspace_bytes(void) { return sizeof(qf::NormState); }
+
+qf_status qf_grad_norm(const qf_param* t, int n, int g_type, double max_norm, float* d_norm,
+                       int64_t* d_step, void* d_workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    if (n < 0) return fail(QF_ERR_INVALID_ARG, "n = %d < 0", n);
+    if (n > 0 && t == nullptr) return fail(QF_ERR_INVALID_ARG, "tensor array is NULL");
+    if (g_type != QF_X_BF16 && g_type != QF_X_F32)
+        return fail(QF_ERR_UNSUPPORTED, "unknown gradient type %d", g_type);
+    if (std::isnan(max_norm)) return fail(QF_ERR_INVALID_ARG, "max_norm is NaN");
+    if (d_norm == nullptr) return fail(QF_ERR_INVALID_ARG, "d_norm is NULL");
+    if (d_workspace == nullptr || workspace_bytes < sizeof(qf::NormState))
+        return fail(QF_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed",
+                    d_workspace ? workspace_bytes : (size_t)0, sizeof(qf::NormState));
+    if (!aligned16(d_workspace)) return fail(QF_ERR_ALIGN, "workspace not 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(d_norm) & 3) || (reinterpret_cast<uintptr_t>(d_step) & 7))
+        return fail(QF_ERR_ALIGN, "d_norm or d_step not aligned to its type");
+    for (int i = 0; i < n; ++i) {
+        if (t[i].numel < 0 || t[i].numel > INT64_MAX / 8)
+            return fail(QF_ERR_SHAPE, "tensor %d: bad numel %lld", i, (long long)t[i].numel);
+        if (t[i].numel > 0 && t[i].g == nullptr) return fail(QF_ERR_INVALID_ARG, "tensor %d: g is NULL", i);
+        if (!aligned16(t[i].g)) return fail(QF_ERR_ALIGN, "tensor %d: g not 16-byte aligned", i);
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    qf::NormState* ws = static_cast<qf::NormState*>(d_workspace);
+    return g_type == QF_X_F32 ? norm_all<float>(t, n, max_norm, d_norm, d_step, ws, s)
+                              : norm_all<uint16_t>(t, n, max_norm, d_norm, d_step, ws, s);
+}
+
+}  // extern "C"

@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <atomic>
 #include <mutex>
@@ -13,12 +11,15 @@
 
 #include "qf.h"
 #include "qf_device.cuh"
+#include "qf_host.cuh"
 #include "qf_lora.cuh"
 
 #ifndef QF_LORA_STEP_TWO_PASS
 #define QF_LORA_STEP_TWO_PASS 0  // LoRA step up to rank 16: 1 = pruned amax + fused NVFP4 pass
 #endif
 #include "qf_oneshot.cuh"
+
+thread_local char qf_host::g_err[512] = "";
 
 namespace {
 
@@ -40,30 +41,13 @@ constexpr int kAmaxU = QF_AMAX_U;
 #define QF_NOALLOC_MAX_GROUPS 4092     // 4 header words + 4092 slots = 16 KB of static scratch
 #endif
 
-thread_local char g_err[512] = "";
-
-qf_status fail(qf_status s, const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_err, sizeof g_err, fmt, ap);
-    va_end(ap);
-    return s;
-}
-
-qf_status cuda_fail(cudaError_t e, const char* what) {
-    return fail(QF_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using qf_host::aligned16;
+using qf_host::cuda_fail;
+using qf_host::fail;
+using qf_host::g_err;
+using qf_host::overlap;
 
 int block_of(qf_format f) { return f == QF_NVFP4 ? 16 : f == QF_MXFP4 ? 32 : 256; }
-
-// Whether the byte ranges [a, a + na) and [b, b + nb) intersect (NULL or empty: no).
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-    if (!a || !b || na <= 0 || nb <= 0) return false;
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
-}
 
 // One tensor's input and outputs must be disjoint (the kernels read x through the
 // non-coherent path and write the outputs in the same pass).  Checked per tensor;

@@ -1,0 +1,77 @@
+// qf_host.cuh -- host-side helpers shared by the library's entry points: the error line
+// of qf_last_error, argument checks and the launch-shape cache.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "qf.h"
+
+namespace qf_host {
+
+// The calling thread's qf_last_error() line (defined in qf_api.cu).
+extern thread_local char g_err[512];
+
+inline qf_status fail(qf_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+inline qf_status cuda_fail(cudaError_t e, const char* what) {
+    return fail(QF_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) intersect (NULL or empty: no).
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    if (!a || !b || na <= 0 || nb <= 0) return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+}
+
+// SM count of the current device and resident CTAs per SM of one kernel.  The queries
+// cost microseconds of host time, so each thread keeps the last answers in a small
+// ring (no allocation).
+struct Shape { int sms; int per_sm; };
+
+template <typename K>
+qf_status shape_of(K kernel, int threads, size_t smem, Shape* out) {
+    struct Entry { const void* kernel; int threads; size_t smem; int dev; Shape s; };
+    constexpr int kEntries = 64;
+    thread_local Entry cache[kEntries];
+    thread_local int used = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const void* key = reinterpret_cast<const void*>(kernel);
+    for (int i = 0; i < std::min(used, kEntries); ++i)
+        if (cache[i].kernel == key && cache[i].threads == threads && cache[i].smem == smem &&
+            cache[i].dev == dev) {
+            *out = cache[i].s;
+            return QF_OK;
+        }
+    Shape s{};
+    e = cudaDeviceGetAttribute(&s.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+    if (smem > 48 * 1024) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    }
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&s.per_sm, kernel, threads, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+    if (s.per_sm < 1) s.per_sm = 1;
+    cache[used % kEntries] = {key, threads, smem, dev, s};
+    used = used + 1 < 2 * kEntries ? used + 1 : kEntries;
+    *out = s;
+    return QF_OK;
+}
+
+}  // namespace qf_host

@@ -385,6 +385,119 @@ qf_status qf_amax_fakequant_lora(const qf_tensor* t, const qf_lora* l, int n,
  * qf_fakequant, qf_pack and qf_ste_backward.
  */
 
+/*
+ * The optimizer step of a training run, over every trained tensor at once: the FP32
+ * latent weights of full-parameter training (qf_tensor.x_type = QF_X_F32 reads them in
+ * the next forward pass), or the BF16 factors of LoRA adapters.
+ *
+ * One tensor of a step.
+ *   p        parameters, numel of qf_adamw_opt.p_type, updated in place
+ *   g        gradient, numel of g_type (as it leaves qf_ste_backward: BF16), not changed
+ *   m, v     states, updated in place; zero before the first step:
+ *              QF_STATE_F32   FP32[numel] each: first and second moment
+ *              QF_STATE_E4M3  one E4M3 byte per element each: first moment, and square
+ *                             root of the second moment
+ *   m_scale, v_scale
+ *            QF_STATE_E4M3: FP32[ceil(numel / 256)] each, one scale per 256 consecutive
+ *            elements (the last block may be short), updated in place; zero before the
+ *            first step.  QF_STATE_F32: ignored.
+ *   w        NULL, or BF16[numel] receiving the updated parameters rounded to BF16 (FP32
+ *            parameters only)
+ *   weight_decay   decoupled weight decay of this tensor (finite, >= 0)
+ *   group    tie group in [0, n_groups) of d_group_amax, or -1: in none.  Ignored when
+ *            d_group_amax is NULL.
+ * p, g, m, v and w are 16-byte aligned (E4M3 states too) and do not overlap.
+ */
+#define QF_STATE_F32 0
+#define QF_STATE_E4M3 1
+#define QF_STATE_BLOCK 256
+typedef struct qf_param {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    void* w;
+    int64_t numel;
+    double weight_decay;
+    int32_t group;
+    int32_t reserved;
+} qf_param;
+
+/*
+ * The step's options, one set for all tensors of the call.
+ *   lr, beta1, beta2, eps   0 <= beta < 1, eps >= 0 (with eps == 0 an element whose
+ *                  gradients were all zero becomes NaN)
+ *   step           number of this step, from 1
+ *   d_lr           NULL, or DEVICE FP32[1] that replaces lr
+ *   d_step         NULL, or DEVICE int64[1] that replaces step
+ *   d_grad_scale   NULL, or DEVICE FP32[1] every gradient is multiplied with
+ *                  (qf_grad_norm's d_norm + 1).  NaN: the step is skipped, every tensor
+ *                  stays as it was.
+ *   p_type, g_type QF_X_BF16 or QF_X_F32;  state  QF_STATE_F32 or QF_STATE_E4M3
+ * The device scalars are read when the call runs on the stream, so a captured step
+ * replays with the values they hold then.
+ */
+typedef struct qf_adamw_opt {
+    double lr, beta1, beta2, eps;
+    int64_t step;
+    const float* d_lr;
+    const int64_t* d_step;
+    const float* d_grad_scale;
+    int32_t p_type;
+    int32_t g_type;
+    int32_t state;
+    int32_t reserved;
+} qf_adamw_opt;
+
+/*
+ * qf_adamw -- one AdamW step (Loshchilov and Hutter, "Decoupled Weight Decay
+ * Regularization") of n tensors in one launch (one per 352 tensors).
+ *
+ * Numerics (IEEE binary32, round to nearest even, no fused multiply-add; b1, 1 - b1, b2,
+ * 1 - b2, eps and the step's constants are formed in binary64 and rounded once):
+ *   g' = scale * g
+ *   m  = m * b1 + g' * (1 - b1)
+ *   v  = v * b2 + (g' * g') * (1 - b2)
+ *   p  = p * (1 - lr*wd) - (m / (sqrt(v) * rs + eps)) * (lr / (1 - b1^step)),
+ *        rs = 1 / sqrt(1 - b2^step)
+ * BF16 parameters are widened, and the result is rounded to BF16.
+ *   QF_STATE_E4M3: m = m_scale * code, v = r * r with r = v_scale * code; after the step,
+ *   per block of 256: scale = amax / 448 (0 if that is below 2^-126), code =
+ *   E4M3(x * (1 / scale)) with x = m, or x = sqrt(v), where a positive x takes at least
+ *   code 1 (unless the scale is 0), so that no divisor falls to eps by rounding.  The
+ *   update itself uses m and v before they are encoded.
+ *   d_group_amax   NULL, or FP32[n_groups]: overwritten with the tie groups' max |p| of the
+ *                  updated parameters (0 for a group with no tensor): the d_group_amax the
+ *                  next forward pass's qf_fakequant needs, without qf_amax_tied's read
+ *                  of the weights.  A skipped step gives that of the unchanged ones.
+ * Gradients and states must be finite for the values above; a NaN or infinite gradient
+ * spreads into its element's (8-bit: its block's) state.  Use qf_grad_norm to skip such
+ * a step.
+ * Errors: as for the other calls; QF_ERR_INVALID_ARG for a NULL p, g, m, v (or, 8-bit, scale)
+ *   of a tensor that is not empty, a beta, eps, lr, step or weight decay out of range, w
+ *   with BF16 parameters, overlapping buffers; QF_ERR_UNSUPPORTED for an unknown type.
+ */
+qf_status qf_adamw(const qf_param* t, int n, const qf_adamw_opt* opt, float* d_group_amax,
+                   int n_groups, void* stream);
+
+/*
+ * qf_grad_norm -- global L2 norm of n gradients and the scale that clips it.
+ *   d_norm[0] = sqrt(sum of g^2 over every element of every tensor), the sum in binary64;
+ *               +inf if an element is infinite or NaN (or the norm exceeds FP32)
+ *   d_norm[1] = min(1, max_norm / norm); 1 if max_norm <= 0 (no clipping) or the norm is 0;
+ *               NaN if d_norm[0] is +inf (qf_adamw then skips the step)
+ *   d_step      NULL, or DEVICE int64[1], advanced by one unless d_norm[0] is +inf
+ *   d_workspace device memory of qf_grad_norm_workspace_bytes() bytes, 16-byte aligned,
+ *               zero before its first use.  Calls that may overlap need their own.
+ * Only g and numel of each tensor are read.  The order of the sum is fixed for a device,
+ * so equal gradients give equal results.  n == 0 gives norm 0.
+ */
+qf_status qf_grad_norm(const qf_param* t, int n, int g_type, double max_norm, float* d_norm,
+                       int64_t* d_step, void* d_workspace, size_t workspace_bytes, void* stream);
+size_t qf_grad_norm_workspace_bytes(void);
+
 /* Static description of a status code. */
 const char* qf_status_string(qf_status s);
 
@@ -395,7 +508,8 @@ const char* qf_last_error(void);
  * reserved field that had to be 0, which still means BF16); 1.2 the LoRA calls;
  * 1.3 QF_Q4K_MSE; 1.4 qf_amax_fakequant, its workspace calls and QF_ERR_TIMEOUT;
  * 1.5 qf_amax_fakequant_noalloc; 1.6 qf_amax_fakequant_lora; 1.7 sticky workspace
- * error flags, qf_noalloc_check and qf_test_barrier_timeout. */
+ * error flags, qf_noalloc_check and qf_test_barrier_timeout.  Calls added since only add
+ * symbols (qf_adamw, qf_grad_norm); nothing that 1.7 declares changed. */
 int qf_version(void);
 
 #ifdef __cplusplus

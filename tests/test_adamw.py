@@ -1,0 +1,447 @@
+"""qf_adamw and qf_grad_norm: refusals on the host; on the GPU, bit-exact parity with the
+documented binary32 steps (numpy, one rounding per operation), closeness to the formula in
+64 bits, guards behind every buffer, skipping, device scalars, graphs and streams."""
+import ctypes
+
+import ml_dtypes
+import numpy as np
+import pytest
+import torch
+
+import fp4_fake_quant_b200 as qf
+
+DEV = "cuda:0"
+F, D = np.float32, np.float64
+E4M3 = ml_dtypes.float8_e4m3fn
+HYPER = dict(lr=3e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1)
+
+
+# ------------------------------------------------------------------ host refusals
+
+def _arr(n=1, **over):
+    arr = (qf.binding.QfParam * n)()
+    for i, t in enumerate(arr):
+        base = 0x1000000 * (i + 1)
+        t.p, t.g, t.m, t.v = base, base + 0x100000, base + 0x200000, base + 0x300000
+        t.m_scale, t.v_scale, t.numel = base + 0x400000, base + 0x500000, 1000
+        for k, v in over.items():
+            setattr(t, k, v)
+    return arr
+
+
+def _opt(**over):
+    o = qf.binding.QfAdamwOpt(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1, p_type=1, g_type=0)
+    for k, v in over.items():
+        setattr(o, k, v)
+    return o
+
+
+@pytest.mark.parametrize("status,arr,opt", [
+    (1, _arr(p=0), {}), (1, _arr(g=0), {}), (1, _arr(m=0), {}), (1, _arr(v=0), {}),
+    (1, _arr(m_scale=0), {"state": 1}), (1, _arr(v_scale=0), {"state": 1}),
+    (2, _arr(numel=-1), {}), (2, _arr(numel=1 << 62), {}),
+    (3, _arr(p=0x1000008), {}), (3, _arr(g=0x1100002), {}), (3, _arr(w=0x1600004), {}),
+    (3, _arr(m_scale=0x1400002), {"state": 1}),
+    (1, _arr(w=0x1600000), {"p_type": 0}),                  # a copy of BF16 parameters
+    (1, _arr(g=0x1000100), {}), (1, _arr(v=0x1200010), {}), (1, _arr(w=0x1000000), {}),
+    (1, _arr(weight_decay=-0.1), {}), (1, _arr(weight_decay=float("nan")), {}),
+    (4, _arr(), {"p_type": 2}), (4, _arr(), {"g_type": -1}), (4, _arr(), {"state": 2}),
+    (1, _arr(), {"beta1": 1.0}), (1, _arr(), {"beta2": -0.1}), (1, _arr(), {"beta2": float("nan")}),
+    (1, _arr(), {"eps": -1.0}), (1, _arr(), {"lr": float("inf")}), (1, _arr(), {"step": 0}),
+])
+def test_step_refusals(status, arr, opt):
+    assert qf.lib.qf_adamw(arr, 1, ctypes.byref(_opt(**opt)), None, 0, None) == status
+    assert qf.lib.qf_last_error()
+
+
+def test_step_refuses_groups_and_null():
+    o = ctypes.byref(_opt())
+    assert qf.lib.qf_adamw(_arr(), 1, None, None, 0, None) == 1
+    assert qf.lib.qf_adamw(None, 1, o, None, 0, None) == 1
+    assert qf.lib.qf_adamw(_arr(), -1, o, None, 0, None) == 1
+    assert qf.lib.qf_adamw(_arr(group=2), 1, o, 0x5000, 2, None) == 1
+    assert qf.lib.qf_adamw(_arr(group=-2), 1, o, 0x5000, 2, None) == 1
+    assert qf.lib.qf_adamw(_arr(), 1, o, 0x5000, 0, None) == 1
+    assert qf.lib.qf_adamw(None, 0, o, None, 0, None) == 0            # nothing to do
+    assert qf.lib.qf_adamw(_arr(numel=0, p=0, g=0, m=0, v=0), 1, o, None, 0, None) == 0
+
+
+def test_norm_refusals():
+    ws, n = 0x9000, qf.lib.qf_grad_norm_workspace_bytes()
+
+    def call(arr=_arr(), count=1, kind=1, out=0x5000, step=None, w=ws, wb=n, most=1.0):
+        return qf.lib.qf_grad_norm(arr, count, kind, most, out, step, w, wb, None)
+    assert call(count=-1) == 1 and call(arr=None) == 1 and call(kind=3) == 4
+    assert call(out=None) == 1 and call(w=None) == 1 and call(wb=n - 1) == 1
+    assert call(w=0x9008) == 3 and call(out=0x5002) == 3 and call(step=0x7004) == 3
+    assert call(arr=_arr(g=0)) == 1 and call(arr=_arr(g=0x1000004)) == 3
+    assert call(arr=_arr(numel=-5)) == 2 and call(most=float("nan")) == 1
+
+
+def test_struct_layouts_match_the_header():
+    assert ctypes.sizeof(qf.binding.QfParam) == 80
+    assert qf.binding.QfParam.group.offset == 72
+    assert ctypes.sizeof(qf.binding.QfAdamwOpt) == 80
+
+
+def test_binding_refusals():
+    p = torch.zeros(4)
+    with pytest.raises(ValueError):                                   # not on a GPU
+        qf.qf_adamw([p], [p], [p], [p], lr=0.1)
+    with pytest.raises(ValueError):                                   # as many gradients as tensors
+        qf.qf_adamw([p], [], [p], [p], lr=0.1)
+    with pytest.raises(TypeError):                                    # two types in one call
+        qf.qf_adamw([p, p.bfloat16()], [p, p], [p, p], [p, p], lr=0.1)
+    with pytest.raises(TypeError):
+        qf.qf_adamw([p.double()], [p], [p], [p], lr=0.1)
+    with pytest.raises(ValueError):                                   # 8-bit states without scales
+        qf.qf_adamw([p], [p], [p.to(torch.uint8)], [p.to(torch.uint8)], lr=0.1)
+    with pytest.raises(ValueError):
+        qf.alloc_adamw_state(p, bits=16)
+
+
+# ------------------------------------------------------------------ the documented steps
+
+def bf16(x):
+    return x.astype(ml_dtypes.bfloat16).astype(F)
+
+
+def blocks(x):
+    room = np.zeros((len(x) + 255) // 256 * 256, x.dtype)
+    room[:len(x)] = x
+    return room.reshape(-1, 256)
+
+
+def encode(x, lift):
+    b = blocks(x)
+    scale = (np.abs(b).max(1) / F(448)).astype(F)
+    scale[scale < F(2.0 ** -126)] = 0
+    inv = np.where(scale > 0, F(1) / np.where(scale > 0, scale, F(1)), F(0)).astype(F)
+    codes = (b * inv[:, None]).astype(E4M3).view(np.uint8)
+    if lift:
+        codes = np.where((codes == 0) & (b > 0) & (scale[:, None] > 0), 1, codes).astype(np.uint8)
+    return codes.reshape(-1)[:len(x)], scale
+
+
+def decode(codes, scale, n):
+    return (blocks(codes).view(E4M3).astype(F) * scale[:, None]).reshape(-1)[:n]
+
+
+def step32(p, g, m, v, t, scale=1.0, lr=3e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, bits=32,
+           ms=None, vs=None, p16=False):
+    """One step as include/qf.h states it."""
+    b1, b2 = betas
+    if bits == 8:
+        m = decode(m, ms, len(p))
+        r = decode(v, vs, len(p))
+        v = r * r
+    g = g * F(scale)
+    m = m * F(b1) + g * F(1 - b1)
+    v = v * F(b2) + (g * g) * F(1 - b2)
+    root = np.sqrt(v)
+    den = root * F(1 / np.sqrt(1 - b2 ** t)) + F(eps)
+    p = p * F(1 - lr * weight_decay) - (m / den) * F(lr / (1 - b1 ** t))
+    if p16:
+        p = bf16(p)
+    if bits == 8:
+        (m, ms), (v, vs) = encode(m, False), encode(root, True)
+    return p, m, v, ms, vs
+
+
+class Case:
+    """Parameters, gradients and states of several tensors on host and device, every device
+    buffer with a guard of 64 bytes behind it."""
+
+    def __init__(self, sizes, p="f32", g="bf16", bits=32, seed=0, zero=0.05):
+        rng = np.random.default_rng(seed)
+        self.bits, self.pt, self.gt, self.sizes = bits, p, g, sizes
+        mk = lambda n, s: (rng.standard_normal(n) * s).astype(F)   # noqa: E731
+        self.p = [mk(n, 0.02) if p == "f32" else bf16(mk(n, 0.02)) for n in sizes]
+        self.g = [(mk(n, 1e-3) * (rng.random(n) > zero)).astype(F) for n in sizes]
+        if g == "bf16":
+            self.g = [bf16(x) for x in self.g]
+        m, r = [mk(n, 3e-4) for n in sizes], [np.abs(mk(n, 1e-3)) for n in sizes]
+        self.ms = self.vs = [None] * len(sizes)
+        if bits == 32:
+            self.m, self.v = m, [x * x for x in r]
+        else:
+            (self.m, self.ms), (self.v, self.vs) = (map(list, zip(*[encode(x, lift) for x in xs]))
+                                                    for xs, lift in ((m, False), (r, True)))
+        self.raw = []
+        typ = {"f32": torch.float32, "bf16": torch.bfloat16}
+        st = torch.float32 if bits == 32 else torch.uint8
+        self.dp, self.dg = self._up(self.p, typ[p]), self._up(self.g, typ[g])
+        self.dm, self.dv = self._up(self.m, st), self._up(self.v, st)
+        self.dms = self._up(self.ms, torch.float32) if bits == 8 else None
+        self.dvs = self._up(self.vs, torch.float32) if bits == 8 else None
+        self.dw = self._up([np.zeros(n, F) for n in sizes], torch.bfloat16)
+
+    def _up(self, xs, dtype):
+        out = []
+        for x in xs:
+            t = torch.from_numpy(np.ascontiguousarray(x)).to(dtype)
+            nb = t.numel() * t.element_size()
+            raw = torch.full((nb + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+            v = raw[:nb].view(dtype)
+            v.copy_(t.view(-1))
+            self.raw.append((raw, nb))
+            out.append(v)
+        return out
+
+    def step(self, t, copies=False, **kw):
+        more = dict(m_scales=self.dms, v_scales=self.dvs) if self.bits == 8 else {}
+        qf.qf_adamw(self.dp, self.dg, self.dm, self.dv, step=t, copies=self.dw if copies else None,
+                    **{**HYPER, **more, **kw})
+
+    def want(self, t, scale=1.0, decays=None, **kw):
+        out = [step32(self.p[i], self.g[i], self.m[i], self.v[i], t, scale, bits=self.bits,
+                      ms=self.ms[i], vs=self.vs[i], p16=self.pt == "bf16",
+                      **{**HYPER, **kw, **({"weight_decay": decays[i]} if decays else {})})
+               for i in range(len(self.sizes))]
+        self.p, self.m, self.v, self.ms, self.vs = map(list, zip(*out))
+
+    def check(self, copies=False):
+        torch.cuda.synchronize()
+        for i, n in enumerate(self.sizes):
+            for name, got, want in (("p", self.dp[i], self.p[i]), ("m", self.dm[i], self.m[i]),
+                                    ("v", self.dv[i], self.v[i])):
+                got = got.float().cpu().numpy() if got.dtype != torch.uint8 else got.cpu().numpy()
+                bad = np.nonzero(got != want)[0]
+                assert bad.size == 0, f"{name}[{i}] ({n}): {bad.size} differ, first {bad[0]}: " \
+                                      f"{got[bad[0]]!r} for {want[bad[0]]!r}"
+            if self.bits == 8:
+                assert np.array_equal(self.dms[i].cpu().numpy(), self.ms[i]), f"m_scale[{i}]"
+                assert np.array_equal(self.dvs[i].cpu().numpy(), self.vs[i]), f"v_scale[{i}]"
+            w = self.dw[i].float().cpu().numpy()
+            assert np.array_equal(w, bf16(self.p[i]) if copies else np.zeros(n, F)), f"w[{i}]"
+        for raw, nb in self.raw:
+            assert bool((raw[nb:] == 0xA5).all()), "wrote past the end of a buffer"
+
+
+RAGGED = [1, 2, 3, 4, 5, 127, 255, 256, 257, 0, 511, 1023, 4097, 65537, 3]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("p", ["f32", "bf16"])
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_steps_are_the_documented_ones_bit_for_bit(p, g, bits):
+    """Three steps over ragged sizes, from warm states."""
+    c = Case(RAGGED, p, g, bits, seed=bits)
+    for t in (1, 2, 1000):
+        c.want(t)
+        c.step(t, copies=p == "f32")
+        c.check(copies=p == "f32")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_from_zero_states_against_64_bits(bits):
+    """Steps from zero states against the formula in binary64.  p: one step rounds at most
+    six times at the size of p or of the update (<= lr + lr wd |p|), 2^-24 each, and the
+    update m / (root rs + eps) has a relative error of at most 10 roundings (m: 3, root: 3,
+    denominator: 2, division and product: 2).  With 8-bit states the second step starts from
+    m and root that are each within 2^-4 relative (E4M3 half step; half of 2^-9 of the block's
+    largest below its normal range): only the first step is compared."""
+    rng = np.random.default_rng(3)
+    n = 5000
+    c = Case([n], "f32", "f32", bits, seed=4)
+    for name in ("dm", "dv"):
+        getattr(c, name)[0].zero_()
+    if bits == 8:
+        c.dms[0].zero_(), c.dvs[0].zero_()
+    p, m, v = c.p[0].astype(D), np.zeros(n), np.zeros(n)
+    lr, (b1, b2), eps, wd = HYPER["lr"], HYPER["betas"], HYPER["eps"], HYPER["weight_decay"]
+    tol = 0.0
+    for t in range(1, 2 if bits == 8 else 6):
+        g = (rng.standard_normal(n) * 10.0 ** rng.integers(-6, 2, n)).astype(F)
+        c.dg[0].copy_(torch.from_numpy(g))
+        g = g.astype(D)
+        m, v = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * g * g
+        up = (m / (1 - b1 ** t)) / (np.sqrt(v / (1 - b2 ** t)) + eps)
+        p = p - lr * up - lr * wd * p
+        # m's terms may cancel: its error is relative to the sum of their magnitudes
+        mag = sum((1 - b1) * b1 ** k for k in range(t)) / (1 - b1 ** t) * np.sqrt(1 / (1 - b2))
+        tol = tol + 2.0 ** -24 * (3 * np.abs(p) + lr * (10 * np.maximum(np.abs(up), mag) + 3))
+        c.step(t)
+        got = c.dp[0].cpu().numpy().astype(D)
+        assert np.all(np.abs(got - p) <= tol), (t, np.max(np.abs(got - p) / tol))
+
+
+@pytest.mark.gpu
+def test_8bit_values_stand_within_half_a_step():
+    """What the codes stand for: m within 2^-4 relative or 2^-10 of the block's largest / 448;
+    a positive root never zero, and at most lifted to the smallest code."""
+    c = Case([256 * 40 + 17], "f32", "f32", 8, seed=9)
+    n = c.sizes[0]
+    g = c.g[0] * 10.0 ** np.random.default_rng(1).integers(-5, 3, n).astype(F)
+    c.g[0] = g.astype(F)
+    c.dg[0].copy_(torch.from_numpy(c.g[0]))
+    m, r = decode(c.m[0], c.ms[0], n), decode(c.v[0], c.vs[0], n)
+    c.step(7)
+    m = 0.9 * m.astype(D) + 0.1 * c.g[0].astype(D)
+    root = np.sqrt(0.95 * r.astype(D) ** 2 + 0.05 * c.g[0].astype(D) ** 2)
+    for x, codes, scale in ((m, c.dm[0], c.dms[0]), (root, c.dv[0], c.dvs[0])):
+        unit = np.repeat(np.abs(blocks(x)).max(1) / 448, 256)[:n]
+        got = decode(codes.cpu().numpy(), scale.cpu().numpy(), n).astype(D)
+        slack = 2.0 ** -21 * np.abs(x) + 2.0 ** -21 * unit       # binary32 along the way
+        half = np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * unit)
+        if x is root:
+            assert np.all(got[x > 0] > 0)
+            half = np.maximum(half, 2.0 ** -9 * unit)
+        assert np.all(np.abs(got - x) <= half + slack)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_extreme_values(bits):
+    """Zero gradients and states, blocks whose 8-bit scale would be below 2^-126, and one
+    block of large values."""
+    c = Case([256 * 5, 300], "f32", "f32", bits, seed=5)
+    g = c.g[0]
+    g[0:256] = 0
+    g[256:512] = F(1e-37)
+    g[512:768] = F(2.0 ** -149)
+    g[768:1024] *= F(1e20)
+    c.g[0], c.dg[0][:] = g, torch.from_numpy(g).to(DEV)
+    for k in ("m", "v"):
+        for host, dev in ((getattr(c, k), getattr(c, "d" + k)),
+                          *(((getattr(c, k + "s"), getattr(c, f"d{k}s")),) if bits == 8 else ())):
+            host[0][:] = 0
+            dev[0].zero_()
+    for t in (1, 2):
+        with np.errstate(under="ignore"):
+            c.want(t)
+        c.step(t)
+        c.check()
+
+
+@pytest.mark.gpu
+def test_many_tensors_take_several_launches_and_decay_alone():
+    sizes = [(37 * i) % 700 + 1 for i in range(800)]
+    c = Case(sizes, "f32", "bf16", 8, seed=6)
+    decays = [0.0 if i % 3 else 0.2 for i in range(800)]
+    groups = [None if i % 5 == 0 else i % 7 for i in range(800)]
+    amax = torch.full((8,), -1.0, device=DEV)
+    c.want(3, decays=decays)
+    c.step(3, weight_decay=decays, groups=groups, group_amax=amax)
+    c.check()
+    want = [max([float(np.abs(c.p[i]).max()) for i in range(800) if groups[i] == k], default=0.0)
+            for k in range(8)]
+    assert amax.tolist() == want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("p", ["f32", "bf16"])
+def test_amax_is_that_of_the_next_forward_pass(p):
+    """The amax of the step is qf_amax_tied's of the updated weights, and stays so when the
+    step is skipped."""
+    c = Case([4096 * 3, 4096, 4096 * 2 + 16], p, "bf16", 32, seed=7)
+    groups, amax, want = [0, 0, 1], torch.empty(2, device=DEV), torch.empty(2, device=DEV)
+    c.step(2, groups=groups, group_amax=amax)
+    qf.qf_amax_tied([x.clone() for x in c.dp], groups, want)
+    assert torch.equal(amax, want)
+    before = [x.clone() for x in c.dp]
+    amax.fill_(-1)
+    c.step(3, groups=groups, group_amax=amax, grad_scale=torch.tensor([float("nan")], device=DEV))
+    assert torch.equal(amax, want) and all(torch.equal(a, b) for a, b in zip(before, c.dp))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_device_scalars_give_the_host_scalars_bits(bits):
+    """lr, step and gradient scale from device memory, also replayed from a graph."""
+    c = Case([1000, 70000], "f32", "bf16", bits, seed=8)
+    lr, step = torch.tensor([7e-4], device=DEV), torch.tensor([41], device=DEV)
+    scale = torch.tensor([0.37], device=DEV)
+    kw = dict(lr_tensor=lr, step_tensor=step, grad_scale=scale, lr=float("nan"))
+    host = float(lr.item())
+    c.want(41, scale=0.37, lr=host)
+    c.step(0, **kw)
+    c.check()
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        c.step(0, **kw)
+    for t, rate, sc in ((42, 5e-4, 1.0), (99999, 1e-5, 0.5)):
+        step.fill_(t), lr.fill_(rate), scale.fill_(sc)
+        graph.replay()
+        c.want(t, scale=sc, lr=float(F(rate)))
+        c.check()
+    scale.fill_(float("nan"))
+    graph.replay()                                               # skipped: nothing changes
+    c.check()
+
+
+# ------------------------------------------------------------------ the gradient norm
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [[1], [7, 0, 9], [4097, 1, 255, 100003], [16] * 1500, [1 << 22]])
+def test_norm_against_64_bits(kind, sizes):
+    """One rounding to binary32 of a binary64 sum (n 2^-53 relative beside it)."""
+    gen = torch.Generator().manual_seed(len(sizes))
+    grads = [torch.randn(n, generator=gen).to(kind) for n in sizes]
+    dev = [g.to(DEV) for g in grads]
+    want = sum(float(g.double().square().sum()) for g in grads) ** 0.5
+    out, ws = torch.empty(2, device=DEV), qf.alloc_grad_norm_workspace(DEV)
+    for most in (0.0, 0.1, 1e9):
+        step = torch.tensor([5], device=DEV)
+        qf.qf_grad_norm(dev, out, max_norm=most, step_tensor=step, workspace=ws)
+        norm, scale = out.tolist()
+        assert abs(norm - want) <= want * 2.0 ** -24 * 1.01
+        clip = min(1.0, most / want) if most > 0 else 1.0
+        assert abs(scale - clip) <= clip * 2.0 ** -24 * 1.01
+        assert step.item() == 6
+        first = out.clone()
+        qf.qf_grad_norm(dev, out, max_norm=most, workspace=ws)    # the workspace is ready again
+        assert torch.equal(first, out)
+
+
+@pytest.mark.gpu
+def test_norm_of_extreme_gradients():
+    out, ws = torch.empty(2, device=DEV), qf.alloc_grad_norm_workspace(DEV)
+    run = lambda *g: (qf.qf_grad_norm(list(g), out, max_norm=1.0, workspace=ws), out.tolist())[1]  # noqa: E731
+    assert run() == [0.0, 1.0]
+    assert run(torch.zeros(1000, device=DEV)) == [0.0, 1.0]
+    assert run(torch.full((4,), 1e38, device=DEV))[0] == pytest.approx(2e38, rel=1e-6)
+    tiny = torch.full((4,), 1e-30, device=DEV)
+    assert run(tiny) == [pytest.approx(2e-30, rel=1e-6), 1.0]
+    step = torch.tensor([5], device=DEV)
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        for kind in (torch.float32, torch.bfloat16):
+            g = torch.ones(5000, device=DEV, dtype=kind)
+            g[4999] = bad
+            qf.qf_grad_norm([torch.ones(3, device=DEV, dtype=kind), g], out, max_norm=1.0,
+                            step_tensor=step, workspace=ws)
+            norm, scale = out.tolist()
+            assert norm == float("inf") and scale != scale and step.item() == 5
+    big = torch.full((8,), 3e38, device=DEV)                     # finite, but the norm is not FP32's
+    assert run(big)[0] == float("inf")
+
+
+@pytest.mark.gpu
+def test_clipped_step_in_a_graph_on_another_stream():
+    """norm -> step, captured once and replayed: the step count moves with the finite norms."""
+    c = Case([5000, 129], "f32", "bf16", 8, seed=11)
+    norm, step = torch.empty(2, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    ws = qf.alloc_grad_norm_workspace(DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        qf.qf_grad_norm(c.dg, norm, max_norm=0.01, step_tensor=step, workspace=ws)
+        c.step(0, step_tensor=step, grad_scale=norm[1:])
+    for t in (1, 2, 3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert step.item() == t
+        total = sum(float((g.astype(D) ** 2).sum()) for g in c.g) ** 0.5
+        assert abs(norm[0].item() - total) <= total * 2.0 ** -24 * 1.01
+        c.want(t, scale=norm[1].item())
+        c.check()
+    c.dg[1][7] = float("nan")
+    graph.replay()
+    torch.cuda.synchronize()
+    assert step.item() == 3
+    c.check()
