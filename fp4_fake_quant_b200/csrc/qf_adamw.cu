@@ -33,7 +33,8 @@ int64_t units_of(int64_t numel) { return (numel + kParamBlock - 1) / kParamBlock
 qf_status check_param(const qf_param& t, int i, const qf_adamw_opt& o, const float* amax,
                       int n_groups) {
     if (t.numel < 0) return fail(QF_ERR_SHAPE, "tensor %d: numel = %lld < 0", i, (long long)t.numel);
-    if (t.numel > INT64_MAX / 8) return fail(QF_ERR_SHAPE, "tensor %d: numel overflows", i);
+    if (t.numel > qf::kParamMaxNumel)
+        return fail(QF_ERR_SHAPE, "tensor %d: numel = %lld is above 2^34", i, (long long)t.numel);
     if (amax && (t.group < -1 || t.group >= n_groups))
         return fail(QF_ERR_INVALID_ARG, "tensor %d: group %d outside [-1, %d)", i, t.group, n_groups);
     if (!(t.weight_decay >= 0.0) || std::isinf(t.weight_decay))
@@ -60,11 +61,11 @@ qf_status check_param(const qf_param& t, int i, const qf_adamw_opt& o, const flo
     return QF_OK;
 }
 
-template <typename PT, typename GT, bool S8, int MAXT>
+template <typename PT, typename GT, typename ST, int MAXT>
 qf_status adam_launch(const qf_param* t, int n, const AdamScalars& h, float* amax, cudaStream_t s) {
     ParamTable<MAXT> P;                         // at most 31 KB
     Shape L;
-    qf_status st = shape_of(qf::k_adamw<PT, GT, S8, MAXT>, kAdamThreads, 0, &L);
+    qf_status st = shape_of(qf::k_adamw<PT, GT, ST, MAXT>, kAdamThreads, 0, &L);
     if (st != QF_OK) return st;
     int k = 0;
     int64_t units = 0;
@@ -80,31 +81,37 @@ qf_status adam_launch(const qf_param* t, int n, const AdamScalars& h, float* ama
         d.w = static_cast<uint16_t*>(t[i].w);
         d.wd = t[i].weight_decay;
         d.numel = t[i].numel;
-        d.unit_begin = units;
+        d.unit_begin = (uint32_t)units;
+        d.whole = (uint32_t)(t[i].numel / kParamBlock);
         d.group = amax ? t[i].group : -1;
         d.pad = 0;
         units += units_of(t[i].numel);
     }
     P.h = h;
     P.n = k;
-    P.total_units = units;
+    P.total_units = (uint32_t)units;
     P.amax = reinterpret_cast<uint32_t*>(amax);
     const int64_t want = (units + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
     const int64_t cap = (int64_t)L.sms * L.per_sm * QF_ADAM_WAVES;
-    qf::k_adamw<PT, GT, S8, MAXT><<<(unsigned)std::min(want, cap), kAdamThreads, 0, s>>>(P);
+    qf::k_adamw<PT, GT, ST, MAXT><<<(unsigned)std::min(want, cap), kAdamThreads, 0, s>>>(P);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? QF_OK : cuda_fail(e, "kernel launch");
 }
 
-// The tensors in launches of at most kLargeP (empty ones are dropped).
-template <typename PT, typename GT, bool S8>
+// The tensors in launches of at most kLargeP and kParamMaxUnits (empty ones are dropped).
+template <typename PT, typename GT, typename ST>
 qf_status adam_all(const qf_param* t, int n, const AdamScalars& h, float* amax, cudaStream_t s) {
     for (int at = 0; at < n;) {
         int end = at, live = 0;
-        while (end < n && live + (t[end].numel > 0) <= kLargeP) live += t[end++].numel > 0;
+        int64_t units = 0;
+        for (; end < n && live + (t[end].numel > 0) <= kLargeP; ++end) {
+            units += units_of(t[end].numel);
+            if (live > 0 && units > qf::kParamMaxUnits) break;
+            live += t[end].numel > 0;
+        }
         qf_status st = QF_OK;
-        if (live > kSmallP) st = adam_launch<PT, GT, S8, kLargeP>(t + at, end - at, h, amax, s);
-        else if (live > 0) st = adam_launch<PT, GT, S8, kSmallP>(t + at, end - at, h, amax, s);
+        if (live > kSmallP) st = adam_launch<PT, GT, ST, kLargeP>(t + at, end - at, h, amax, s);
+        else if (live > 0) st = adam_launch<PT, GT, ST, kSmallP>(t + at, end - at, h, amax, s);
         if (st != QF_OK) return st;
         at = end;
     }
@@ -114,8 +121,8 @@ qf_status adam_all(const qf_param* t, int n, const AdamScalars& h, float* amax, 
 template <typename PT, typename GT>
 qf_status adam_states(const qf_param* t, int n, int state, const AdamScalars& h, float* amax,
                       cudaStream_t s) {
-    return state == QF_STATE_E4M3 ? adam_all<PT, GT, true>(t, n, h, amax, s)
-                                  : adam_all<PT, GT, false>(t, n, h, amax, s);
+    return state == QF_STATE_E4M3 ? adam_all<PT, GT, uint8_t>(t, n, h, amax, s)
+                                  : adam_all<PT, GT, float>(t, n, h, amax, s);
 }
 
 constexpr int kSmallN = 16, kLargeN = 1024;       // 24-byte entries: 24 KB of kernel parameters

@@ -15,6 +15,14 @@
 // Layout: a warp takes one 256-element block at a time, two 4-element vectors per lane,
 // so every FP32 access is a whole 512-byte warp transaction, a block's scale is one
 // warp reduction (redux.sync on the bit patterns) and no shared memory is needed.
+// Measured on a B200 (copy: 6.55 TB/s), 142.6M FP32 parameters, BF16 gradients:
+//   FP32 states + BF16 copy   630 us, 6.34 TB/s.  Two CTAs of 8 warps per SM; with three
+//     (fewer registers, more loads in flight) 672 us, and with many short CTAs 702 us.
+//   8-bit states              360 us, 5.56 TB/s.  Issue-bound: 66 instructions per element
+//     for 14 bytes.  It came from 647 us (88 instructions, a branch in every root and
+//     quotient) by branch-free roots and quotients in pairs (455), whole-block addressing
+//     without per-element bounds (386), 32-bit quad indices (360).  Loading a warp's next
+//     block before working on this one: 407 -> 360 us with three CTAs.
 #pragma once
 
 #include <cstdint>
@@ -37,10 +45,13 @@ struct DevParam {
     uint16_t* w;
     double wd;
     int64_t numel;
-    int64_t unit_begin;
+    uint32_t unit_begin;                 // the tensor's first unit (256-element block) of the launch
+    uint32_t whole;                      // how many of its blocks are whole
     int32_t group;
     int32_t pad;
 };
+constexpr int64_t kParamMaxNumel = int64_t(1) << 34;   // a lane's quad index fits 32 bits
+constexpr int64_t kParamMaxUnits = int64_t(1) << 30;   // units of one launch
 
 // Scalars of one step.  ss and rs2 are the host's when the step number and the learning
 // rate came by value; otherwise each CTA forms them from d_step / d_lr, by the same
@@ -59,7 +70,7 @@ template <int MAXT>
 struct ParamTable {
     DevParam t[MAXT];
     AdamScalars h;
-    int64_t total_units;
+    uint32_t total_units;
     uint32_t* amax;                      // per tie group, FP32 bits; NULL: not wanted
     int n;
 };
@@ -78,69 +89,56 @@ __host__ __device__ inline void adam_step_scalars(double lr, double beta1, doubl
 
 #ifdef __CUDACC__
 
-// ---- vectors of four elements at element offset e; n = elements left (>= 4: whole)
-__device__ __forceinline__ void load4(const float* p, int64_t e, int64_t n, float* x) {
-    if (n >= 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p + e);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+// ---- four consecutive elements as they lie in memory: FP32, BF16, or E4M3 codes
+template <typename T> struct Quad;
+template <> struct Quad<float> { using V = float4; };
+template <> struct Quad<uint16_t> { using V = uint2; };
+template <> struct Quad<uint8_t> { using V = uint32_t; };
+
+__device__ __forceinline__ void put(float4& v, int i, float x) { (&v.x)[i] = x; }
+__device__ __forceinline__ void put(uint2& v, int i, uint16_t x) {
+    (i < 2 ? v.x : v.y) |= (uint32_t)x << (16 * (i & 1));
+}
+__device__ __forceinline__ void put(uint32_t& v, int i, uint8_t x) { v |= (uint32_t)x << (8 * i); }
+__device__ __forceinline__ float take(const float4& v, int i) { return (&v.x)[i]; }
+__device__ __forceinline__ uint16_t take(const uint2& v, int i) {
+    return (uint16_t)((i < 2 ? v.x : v.y) >> (16 * (i & 1)));
+}
+__device__ __forceinline__ uint8_t take(uint32_t v, int i) { return (uint8_t)(v >> (8 * i)); }
+
+// Quad q of p, elements 4q .. 4q+3.  WHOLE: all inside the tensor; otherwise n of them are
+// (the others read as 0 and are not written).
+template <bool WHOLE, typename T>
+__device__ __forceinline__ typename Quad<T>::V load_quad(const T* p, uint32_t q, int64_t n) {
+    using V = typename Quad<T>::V;
+    if constexpr (WHOLE) {
+        return reinterpret_cast<const V*>(p)[q];
     } else {
+        V v{};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = i < n ? p[e + i] : 0.0f;
+        for (int i = 0; i < 4; ++i)
+            if (i < n) put(v, i, p[4 * (int64_t)q + i]);
+        return v;
     }
 }
-__device__ __forceinline__ void load4(const uint16_t* p, int64_t e, int64_t n, float* x) {
-    if (n >= 4) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p + e);
-        x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void store_quad(T* p, uint32_t q, int64_t n, typename Quad<T>::V v) {
+    if constexpr (WHOLE) {
+        reinterpret_cast<typename Quad<T>::V*>(p)[q] = v;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            x[i] = i < n ? __uint_as_float((uint32_t)p[e + i] << 16) : 0.0f;
+            if (i < n) p[4 * (int64_t)q + i] = take(v, i);
     }
 }
-__device__ __forceinline__ uint32_t pack_bf16(float hi, float lo) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+__device__ __forceinline__ void widen4(float4 v, float* x) {
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
-__device__ __forceinline__ void store4(float* p, int64_t e, int64_t n, const float* x) {
-    if (n >= 4) {
-        *reinterpret_cast<float4*>(p + e) = make_float4(x[0], x[1], x[2], x[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) p[e + i] = x[i];
-    }
+__device__ __forceinline__ void widen4(uint2 v, float* x) {
+    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
-__device__ __forceinline__ void store4(uint16_t* p, int64_t e, int64_t n, const float* x) {
-    const uint32_t lo = pack_bf16(x[1], x[0]), hi = pack_bf16(x[3], x[2]);
-    if (n >= 4) {
-        *reinterpret_cast<uint2*>(p + e) = make_uint2(lo, hi);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) p[e + i] = (uint16_t)((i < 2 ? lo : hi) >> (16 * (i & 1)));
-    }
-}
-__device__ __forceinline__ uint32_t load_codes4(const uint8_t* p, int64_t e, int64_t n) {
-    if (n >= 4) return *reinterpret_cast<const uint32_t*>(p + e);
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) c |= (uint32_t)p[e + i] << (8 * i);
-    return c;
-}
-__device__ __forceinline__ void store_codes4(uint8_t* p, int64_t e, int64_t n, uint32_t c) {
-    if (n >= 4) {
-        *reinterpret_cast<uint32_t*>(p + e) = c;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) p[e + i] = (uint8_t)(c >> (8 * i));
-}
-__device__ __forceinline__ void decode_e4m3x4(uint32_t c, float* x) {
+__device__ __forceinline__ void widen4(uint32_t c, float* x) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         uint32_t h2;
@@ -150,23 +148,117 @@ __device__ __forceinline__ void decode_e4m3x4(uint32_t c, float* x) {
             : "=f"(x[2 * i]), "=f"(x[2 * i + 1]) : "r"(h2));
     }
 }
+__device__ __forceinline__ uint32_t pack_bf16(float hi, float lo) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float4 narrow4(const float* x, float) { return make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ uint2 narrow4(const float* x, uint16_t) {
+    return make_uint2(pack_bf16(x[1], x[0]), pack_bf16(x[3], x[2]));
+}
 __device__ __forceinline__ uint32_t encode_e4m3x4(const float* x) {
     unsigned short lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-// A block's scale from the bits of its largest magnitude, and the reciprocal its elements
-// are multiplied with.  Below 2^-126 the reciprocal would overflow: the block is zero.
-__device__ __forceinline__ float state_scale(uint32_t amax_bits, float* inv) {
-    float s = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
+// max that keeps a NaN (the scales of a block with a NaN are NaN, not silently finite)
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Two binary32 operations per instruction (fma/mul.rn.f32x2), each rounded once.  There is
+// no paired add here: the code generator fuses a paired product and a paired add into one
+// rounding, whatever the .rn says, so every product that is added to something is added
+// by scalar __fadd_rn.  Products with a constant stay scalar too: a pair of equal
+// constants costs two moves at each use, a scalar operand comes from the constant bank.
+struct F2 {
+    uint64_t d;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float lo, float hi) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    }
+    __device__ __forceinline__ explicit F2(float both) : F2(both, both) {}
+    __device__ __forceinline__ void get(float& lo, float& hi) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+    }
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.d) : "l"(a.d), "l"(b.d));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.d) : "l"(a.d), "l"(b.d), "l"(c.d));
+    return r;
+}
+
+// Square root and quotient of pairs, correctly rounded without a branch: the hardware's
+// approximation, one Newton step, and corrections by the exact remainder (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+// Valid where no step leaves the normal range: StepRange says when that holds.  The
+// compiler's own sequences test and branch per element, which serialises a lane's eight
+// elements, and cannot be paired.
+__device__ __forceinline__ F2 sqrt_normal(F2 v) {
+    float v0, v1, y0, y1, s0, s1, h0, h1;
+    v.get(v0, v1);
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v0));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v1));
+    F2 s = mul2(v, F2(y0, y1));
+    s.get(s0, s1);
+    h0 = __fmul_rn(0.5f, y0);
+    h1 = __fmul_rn(0.5f, y1);
+    const F2 r(__fmaf_rn(-h0, s0, 0.5f), __fmaf_rn(-h1, s1, 0.5f));
+    F2 h(h0, h1);
+    s = fma2(s, r, s);
+    h = fma2(h, r, h);
+    s.get(s0, s1);
+    return fma2(F2(__fmaf_rn(-s0, s0, v0), __fmaf_rn(-s1, s1, v1)), h, s);
+}
+// a / b with nb = -b; a not zero
+__device__ __forceinline__ F2 div_normal(F2 a, F2 nb) {
+    float b0, b1, y0, y1;
+    nb.get(b0, b1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(-b0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(-b1));
+    F2 y(y0, y1);
+    y = fma2(F2(__fmaf_rn(b0, y0, 1.0f), __fmaf_rn(b1, y1, 1.0f)), y, y);
+    F2 q = mul2(a, y);
+    q = fma2(fma2(nb, q, a), y, q);
+    return fma2(fma2(nb, q, a), y, q);
+}
+// Whether every v of a lane lies in [2^-100, 2^20] and every |m| in [2^-100, 2^60].  With
+// rs2 <= 2^10 and eps <= 2^10 (uniform) the divisor is then in [2^-50, 2^21], the quotient
+// in [2^-121, 2^110], and every remainder a multiple of 2^-149.
+struct StepRange {
+    float vlo, vhi, mlo, mhi;
+    __device__ __forceinline__ StepRange() : vlo(1.0f), vhi(0.0f), mlo(1.0f), mhi(0.0f) {}
+    __device__ __forceinline__ void add(float m, float v) {
+        vlo = fminf(vlo, v);
+        vhi = max_nan(vhi, v);
+        mlo = fminf(mlo, fabsf(m));
+        mhi = max_nan(mhi, fabsf(m));
+    }
+    __device__ __forceinline__ bool ok() const {
+        return fminf(vlo, mlo) >= 0x1p-100f && vhi <= 0x1p20f && mhi <= 0x1p60f;
+    }
+};
+
+// A block's scale from its largest magnitude, and the reciprocal its elements are
+// multiplied with.  Below 2^-126 the reciprocal would overflow: the block is zero.
+__device__ __forceinline__ float state_scale(float amax, float* inv) {
+    float s = __fdiv_rn(amax, 448.0f);
     if (s < 0x1p-126f) s = 0.0f;
     *inv = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
     return s;
 }
 
 template <int MAXT>
-__device__ __forceinline__ int param_of_unit(const ParamTable<MAXT>& P, int64_t u) {
+__device__ __forceinline__ int param_of_unit(const ParamTable<MAXT>& P, uint32_t u) {
     int lo = 0, hi = P.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -175,10 +267,67 @@ __device__ __forceinline__ int param_of_unit(const ParamTable<MAXT>& P, int64_t 
     return lo;
 }
 
-// One AdamW step.  PT/GT: float or uint16_t (BF16) parameters and gradients; S8: 8-bit
-// states.  A NaN gradient scale leaves every tensor as it was (the amax is still formed).
-template <typename PT, typename GT, bool S8, int MAXT>
-__global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ ParamTable<MAXT> P) {
+// What a lane holds of one block before it is worked on.
+template <typename PT, typename GT, typename ST>
+struct BlockRaw {
+    typename Quad<PT>::V p[2];
+    typename Quad<GT>::V g[2];
+    typename Quad<ST>::V m[2], v[2];
+    float sm, sv;
+    template <bool WHOLE>
+    __device__ __forceinline__ void load_as(const DevParam& T, uint32_t blk, int lane, bool states) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t q = blk * 64 + lane + 32 * c;
+            const int64_t n = T.numel - 4 * (int64_t)q;
+            p[c] = load_quad<WHOLE>(static_cast<const PT*>(T.p), q, n);
+            if (!states) continue;
+            g[c] = load_quad<WHOLE>(static_cast<const GT*>(T.g), q, n);
+            m[c] = load_quad<WHOLE>(static_cast<const ST*>(T.m), q, n);
+            v[c] = load_quad<WHOLE>(static_cast<const ST*>(T.v), q, n);
+        }
+    }
+    __device__ __forceinline__ void load(const DevParam& T, uint32_t blk, int lane, bool states) {
+        if (blk < T.whole) load_as<true>(T, blk, lane, states);
+        else load_as<false>(T, blk, lane, states);
+        if (sizeof(ST) == 1 && states) {
+            sm = T.ms[blk];
+            sv = T.vs[blk];
+        }
+    }
+};
+
+// What a lane writes of one block.
+template <bool WHOLE, typename PT, typename ST>
+__device__ __forceinline__ void store_block(const DevParam& T, uint32_t q0, const typename Quad<PT>::V* x,
+                                            const float* w, const typename Quad<ST>::V* m,
+                                            const typename Quad<ST>::V* v) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t q = q0 + 32 * c;
+        const int64_t n = T.numel - 4 * (int64_t)q;
+        store_quad<WHOLE>(static_cast<PT*>(T.p), q, n, x[c]);
+        store_quad<WHOLE>(static_cast<ST*>(T.m), q, n, m[c]);
+        store_quad<WHOLE>(static_cast<ST*>(T.v), q, n, v[c]);
+        if (T.w) store_quad<WHOLE>(T.w, q, n, narrow4(w + 4 * c, uint16_t{}));
+    }
+}
+
+#ifndef QF_ADAM_MINB
+#define QF_ADAM_MINB 3          // 8-bit states: resident CTAs asked of the register allocator
+#endif
+#ifndef QF_ADAM_PREFETCH
+#define QF_ADAM_PREFETCH 1      // 8-bit states: load a warp's next block before working on this one
+#endif
+
+// One AdamW step.  PT/GT: float or uint16_t (BF16) parameters and gradients; ST: float or
+// uint8_t (E4M3) states.  A NaN gradient scale leaves every tensor as it was (the amax is
+// still formed).
+template <typename PT, typename GT, typename ST, int MAXT>
+__global__ void __launch_bounds__(kAdamThreads, sizeof(ST) == 1 ? QF_ADAM_MINB : 2)
+k_adamw(const __grid_constant__ ParamTable<MAXT> P) {
+    constexpr bool S8 = sizeof(ST) == 1;
+    constexpr bool kAhead = S8 && QF_ADAM_PREFETCH;
     __shared__ float sh[2];
     const int lane = threadIdx.x & 31;
     const AdamScalars& h = P.h;
@@ -195,130 +344,164 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
     const float gs = h.d_grad_scale ? *h.d_grad_scale : 1.0f;
     const bool skip = gs != gs;
     if (skip && !P.amax) return;
+    const bool mild = rs2 <= 0x1p10f && h.eps <= 0x1p10f;
 
-    const int64_t stride = (int64_t)gridDim.x * (kAdamThreads / 32);
-    int64_t u = (int64_t)blockIdx.x * (kAdamThreads / 32) + (threadIdx.x >> 5);
-    int ti = -1;
-    int64_t end = 0;
-    float keep = 1.0f;
-    uint32_t amax = 0;
-    int amax_group = -1;
-    for (; u < P.total_units; u += stride) {
-        if (u >= end) {
+    const uint32_t stride = gridDim.x * (kAdamThreads / 32);
+    uint32_t u = blockIdx.x * (kAdamThreads / 32) + (threadIdx.x >> 5);
+    if (u >= P.total_units) return;
+    int ti = param_of_unit(P, u);
+    uint32_t end = ti + 1 < P.n ? P.t[ti + 1].unit_begin : P.total_units;
+    float keep = (float)(1.0 - lr * P.t[ti].wd);
+    float amax = 0.0f;
+    int group = P.t[ti].group;
+    BlockRaw<PT, GT, ST> next;
+    if (kAhead) next.load(P.t[ti], u - P.t[ti].unit_begin, lane, !skip);
+    while (true) {
+        const DevParam& T = P.t[ti];
+        const uint32_t blk = u - T.unit_begin;
+        BlockRaw<PT, GT, ST> raw;
+        if (kAhead) raw = next; else raw.load(T, blk, lane, !skip);
+        u += stride;
+        const bool more = u < P.total_units, hop = u >= end;
+        if (more && hop) {
             ti = param_of_unit(P, u);
             end = ti + 1 < P.n ? P.t[ti + 1].unit_begin : P.total_units;
-            keep = (float)(1.0 - lr * P.t[ti].wd);
-            if (P.amax && P.t[ti].group != amax_group) {
-                amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-                if (lane == 0 && amax) atomicMax(P.amax + amax_group, amax);
-                amax = 0;
-                amax_group = P.t[ti].group;
-            }
         }
-        const DevParam& T = P.t[ti];
-        const int64_t blk = u - T.unit_begin;
-        const int64_t e[2] = {blk * kParamBlock + lane * 4, blk * kParamBlock + 128 + lane * 4};
-        PT* const p = static_cast<PT*>(T.p);
-        float x[8], g[8], m[8], v[8];
-        float sm = 0.0f, sv = 0.0f;
-        uint32_t cm[2], cv[2];
-        if (S8 && !skip) {
-            sm = T.ms[blk];
-            sv = T.vs[blk];
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int64_t n = T.numel - e[c];
-            load4(p, e[c], n, x + 4 * c);
-            if (skip) continue;
-            load4(static_cast<const GT*>(T.g), e[c], n, g + 4 * c);
-            if (S8) {
-                cm[c] = load_codes4(static_cast<const uint8_t*>(T.m), e[c], n);
-                cv[c] = load_codes4(static_cast<const uint8_t*>(T.v), e[c], n);
-            } else {
-                load4(static_cast<const float*>(T.m), e[c], n, m + 4 * c);
-                load4(static_cast<const float*>(T.v), e[c], n, v + 4 * c);
-            }
-        }
+        if (kAhead && more) next.load(P.t[ti], u - P.t[ti].unit_begin, lane, !skip);
+
+        const uint32_t q0 = blk * 64 + lane;
+        const bool whole = blk < T.whole;
+        float x[8];
+        widen4(raw.p[0], x);
+        widen4(raw.p[1], x + 4);
         if (!skip) {
-            uint32_t am = 0, av = 0;
+            float g[8], m[8], v[8];
+            StepRange range;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (S8) {
-                    decode_e4m3x4(cm[c], m + 4 * c);
-                    decode_e4m3x4(cv[c], v + 4 * c);
-                }
+            for (int c = 0; c < 2; ++c) {
+                widen4(raw.g[c], g + 4 * c);
+                widen4(raw.m[c], m + 4 * c);
+                widen4(raw.v[c], v + 4 * c);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 8; i += 2) {
+                F2 m2(m[i], m[i + 1]), v2(v[i], v[i + 1]);
                 if (S8) {
-                    m[i] = __fmul_rn(m[i], sm);
-                    const float r = __fmul_rn(v[i], sv);
-                    v[i] = __fmul_rn(r, r);
+                    m2 = mul2(m2, F2(raw.sm));
+                    v2 = mul2(v2, F2(raw.sv));
+                    v2 = mul2(v2, v2);
                 }
-                const float gi = __fmul_rn(g[i], gs);
-                m[i] = __fadd_rn(__fmul_rn(m[i], h.b1), __fmul_rn(gi, h.omb1));
-                v[i] = __fadd_rn(__fmul_rn(v[i], h.b2), __fmul_rn(__fmul_rn(gi, gi), h.omb2));
-                const float root = __fsqrt_rn(v[i]);
-                const float den = __fadd_rn(__fmul_rn(root, rs2), h.eps);
-                x[i] = __fsub_rn(__fmul_rn(x[i], keep), __fmul_rn(__fdiv_rn(m[i], den), ss));
-                if (S8) {
-                    v[i] = root;
-                    am = max(am, __float_as_uint(m[i]) & 0x7FFFFFFFu);
-                    av = max(av, __float_as_uint(root));
+                g[i] = __fmul_rn(g[i], gs);
+                g[i + 1] = __fmul_rn(g[i + 1], gs);
+                F2 gg(g[i], g[i + 1]);
+                gg = mul2(gg, gg);
+                float q[2];
+                gg.get(q[0], q[1]);
+                m2.get(m[i], m[i + 1]);
+                v2.get(v[i], v[i + 1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    m[i + k] = __fadd_rn(__fmul_rn(m[i + k], h.b1), __fmul_rn(g[i + k], h.omb1));
+                    v[i + k] = __fadd_rn(__fmul_rn(v[i + k], h.b2), __fmul_rn(q[k], h.omb2));
+                    range.add(m[i + k], v[i + k]);
                 }
             }
-            if (S8) {
-                // elements behind the tensor's end are zero throughout: m = root = 0
-                float im, iv;
-                sm = state_scale(__reduce_max_sync(0xFFFFFFFFu, am), &im);
-                sv = state_scale(__reduce_max_sync(0xFFFFFFFFu, av), &iv);
+            // p's update; 8-bit states go on with v's root
+            if (mild && range.ok()) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const F2 r = sqrt_normal(F2(v[i], v[i + 1]));
+                    float r0, r1, q0, q1;
+                    r.get(r0, r1);
+                    const F2 nden(__fadd_rn(__fmul_rn(r0, -rs2), -h.eps),
+                                  __fadd_rn(__fmul_rn(r1, -rs2), -h.eps));
+                    div_normal(F2(m[i], m[i + 1]), nden).get(q0, q1);
+                    x[i] = __fsub_rn(__fmul_rn(x[i], keep), __fmul_rn(q0, ss));
+                    x[i + 1] = __fsub_rn(__fmul_rn(x[i + 1], keep), __fmul_rn(q1, ss));
+                    if (S8) {
+                        v[i] = r0;
+                        v[i + 1] = r1;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float r = __fsqrt_rn(v[i]);
+                    const float q = __fdiv_rn(m[i], __fadd_rn(__fmul_rn(r, rs2), h.eps));
+                    x[i] = __fsub_rn(__fmul_rn(x[i], keep), __fmul_rn(q, ss));
+                    if (S8) v[i] = r;
+                }
+            }
+            typename Quad<ST>::V cm[2], cv[2];
+            if constexpr (S8) {
+                // elements behind the tensor's end are zero throughout: m = root = 0.  The
+                // largest root is the root of the largest v.
+                float sm, sv, im, iv;
+                const float mtop = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(range.mhi)));
+                const float vtop = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(range.vhi)));
+                if (fminf(mtop, vtop) >= 0x1p-60f && max_nan(mtop, vtop) <= 0x1p60f) {   // uniform
+                    float top, none;
+                    sqrt_normal(F2(vtop)).get(top, none);
+                    const F2 s = div_normal(F2(mtop, top), F2(-448.0f));
+                    s.get(sm, sv);
+                    div_normal(F2(1.0f), F2(-sm, -sv)).get(im, iv);
+                } else {
+                    sm = state_scale(mtop, &im);
+                    sv = state_scale(__fsqrt_rn(vtop), &iv);
+                }
                 if (lane == 0) {
                     T.ms[blk] = sm;
                     T.vs[blk] = sv;
                 }
+                const float least = iv > 0.0f ? 0x1p-9f : 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float y[4], z[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[i] = __fmul_rn(m[4 * c + i], im);
-                        z[i] = __fmul_rn(v[4 * c + i], iv);
+                    for (int i = 0; i < 4; i += 2) {
+                        const int k = 4 * c + i;
+                        mul2(F2(m[k], m[k + 1]), F2(im)).get(y[i], y[i + 1]);
+                        mul2(F2(v[k], v[k + 1]), F2(iv)).get(z[i], z[i + 1]);
                         // a positive root takes at least the smallest code, 2^-9
-                        if (v[4 * c + i] > 0.0f && iv > 0.0f) z[i] = fmaxf(z[i], 0x1p-9f);
+                        z[i] = max_nan(z[i], v[k] > 0.0f ? least : 0.0f);
+                        z[i + 1] = max_nan(z[i + 1], v[k + 1] > 0.0f ? least : 0.0f);
                     }
                     cm[c] = encode_e4m3x4(y);
                     cv[c] = encode_e4m3x4(z);
                 }
-            }
+            } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int64_t n = T.numel - e[c];
-                store4(p, e[c], n, x + 4 * c);
-                if (S8) {
-                    store_codes4(static_cast<uint8_t*>(T.m), e[c], n, cm[c]);
-                    store_codes4(static_cast<uint8_t*>(T.v), e[c], n, cv[c]);
-                } else {
-                    store4(static_cast<float*>(T.m), e[c], n, m + 4 * c);
-                    store4(static_cast<float*>(T.v), e[c], n, v + 4 * c);
+                for (int c = 0; c < 2; ++c) {
+                    cm[c] = narrow4(m + 4 * c, 0.0f);
+                    cv[c] = narrow4(v + 4 * c, 0.0f);
                 }
-                if (T.w) store4(T.w, e[c], n, x + 4 * c);
+            }
+            const typename Quad<PT>::V px[2] = {narrow4(x, PT{}), narrow4(x + 4, PT{})};
+            if (whole) store_block<true, PT, ST>(T, q0, px, x, cm, cv);
+            else store_block<false, PT, ST>(T, q0, px, x, cm, cv);
+            if (sizeof(PT) == 2) {                    // the amax is of the weights as kept
+                widen4(px[0], x);
+                widen4(px[1], x + 4);
             }
         }
-        if (P.amax && amax_group >= 0) {
+        if (group >= 0) {
+            if (whole) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+                for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(x[i]));
+            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float y = x[4 * c + i];
-                    if (sizeof(PT) == 2)     // the amax is that of the weights as they are kept
-                        y = __uint_as_float(pack_bf16(0.0f, y) << 16);
-                    if (e[c] + i < T.numel) amax = max(amax, __float_as_uint(y) & 0x7FFFFFFFu);
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (4 * (int64_t)(q0 + 32 * (i / 4)) + (i & 3) < T.numel) amax = max_nan(amax, fabsf(x[i]));
+            }
         }
-    }
-    if (P.amax) {
-        amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-        if (lane == 0 && amax) atomicMax(P.amax + amax_group, amax);
+        if (!more || P.t[ti].group != group) {
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax));
+            if (group >= 0 && lane == 0 && top) atomicMax(P.amax + group, top);
+            amax = 0.0f;
+            group = P.t[ti].group;
+        }
+        if (!more) break;
+        if (hop) keep = (float)(1.0 - lr * P.t[ti].wd);
     }
 }
 

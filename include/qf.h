@@ -391,7 +391,7 @@ qf_status qf_amax_fakequant_lora(const qf_tensor* t, const qf_lora* l, int n,
  * the next forward pass), or the BF16 factors of LoRA adapters.
  *
  * One tensor of a step.
- *   p        parameters, numel of qf_adamw_opt.p_type, updated in place
+ *   p        parameters, numel (<= 2^34) of qf_adamw_opt.p_type, updated in place
  *   g        gradient, numel of g_type (as it leaves qf_ste_backward: BF16), not changed
  *   m, v     states, updated in place; zero before the first step:
  *              QF_STATE_F32   FP32[numel] each: first and second moment

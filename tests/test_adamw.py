@@ -445,3 +445,44 @@ def test_clipped_step_in_a_graph_on_another_stream():
     torch.cuda.synchronize()
     assert step.item() == 3
     c.check()
+
+
+# ------------------------------------------------------------------ the kernel's own root and quotient
+
+def _quotients(m, v):
+    """m / sqrt(v) as one step computes it: halving betas undo themselves exactly, no decay, no
+    eps, step large enough that the bias corrections are 1; p = 0 - 1 * (m / sqrt(v))."""
+    p, g = torch.zeros(len(m), device=DEV), torch.zeros(len(m), device=DEV)
+    dm, dv = torch.from_numpy(m * F(2)).to(DEV), torch.from_numpy(v * F(2)).to(DEV)
+    qf.qf_adamw([p], [g], [dm], [dv], lr=1.0, step=2000, betas=(0.5, 0.5), eps=0.0, weight_decay=0.0)
+    assert np.array_equal(dm.cpu().numpy(), m) and np.array_equal(dv.cpu().numpy(), v)
+    return -p.cpu().numpy()
+
+
+@pytest.mark.gpu
+def test_roots_are_correctly_rounded_on_every_mantissa():
+    """Every binary32 value of [1, 4): all mantissas at both exponent parities.  m = sqrt(v)
+    rounded, so the quotient is 1 only where the kernel's root is exactly that."""
+    v = np.arange(0x3F800000, 0x40800000, dtype=np.uint32).view(F)
+    assert np.all(_quotients(np.sqrt(v), v) == 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(3))
+def test_quotients_are_correctly_rounded(seed):
+    """Random mantissas over the exponents of the fast path and beyond both its ends, and
+    divisors next to powers of two, where an approximate reciprocal is worst."""
+    rng = np.random.default_rng(seed)
+    n = 1 << 22
+    m = ((1 + rng.random(n)) * 2.0 ** rng.uniform(-110, 62, n) * rng.choice([-1, 1], n)).astype(F)
+    v = ((1 + rng.random(n)) * 2.0 ** rng.uniform(-104, 24, n)).astype(F)
+    if seed == 1:
+        m = ((1 + rng.random(n)) * rng.choice([-1, 1], n)).astype(F)
+        v = (F(1) - rng.integers(0, 64, n).astype(F) * F(2.0 ** -24)) ** 2
+        v = np.where(rng.random(n) < 0.5, v, 1 / v).astype(F)
+    if seed == 2:
+        m[rng.random(n) < 0.001] = 0
+        v[rng.random(n) < 0.001] = F(2.0 ** -149)
+    with np.errstate(all="ignore"):
+        want = m / np.sqrt(v)
+    assert np.array_equal(_quotients(m, v), want)
