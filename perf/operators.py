@@ -358,17 +358,15 @@ def _lora_own(s):
         one = case["adapters"] == 1 and not case["bare"]       # every token has the adapter
         s["plan"] = None if one else qf.alloc_lora_plan(case["tokens"], case["adapters"], DEV)
         s["u"] = qf.alloc_lora_u(case["tokens"], s["adapters"])
-        work = qf.alloc_lora_workspace(case["tokens"], s["adapters"], backward=train)
         if not one:
             s["plan_call"] = qf.prepare_lora_plan(s["index"], case["adapters"], s["plan"])
-        s["call"] = qf.prepare_lora_apply(s["x"], s["adapters"], s["y"], s["u"], plan=s["plan"],
-                                          workspace=work)
+        s["call"] = qf.prepare_lora_apply(s["x"], s["adapters"], s["y"], s["u"], plan=s["plan"])
         if train:
             s["ga"] = [torch.empty_like(a) for _, a, _ in s["adapters"]]
             s["gb"] = [torch.empty_like(b) for b, _, _ in s["adapters"]]
             s["back"] = qf.prepare_lora_apply_backward(
                 s["x"], s["gy"], s["adapters"], s["u"], s["gx"], s["ga"], s["gb"],
-                plan=s["plan"], workspace=work)
+                plan=s["plan"], workspace=qf.alloc_lora_workspace(case["tokens"], s["adapters"]))
     if s["plan"] is not None:
         s["plan_call"]()
     s["call"]()
