@@ -13,7 +13,10 @@ from .binding import (QF_MXFP4, QF_NVFP4, QF_Q4K, QF_X_BF16, QF_X_F32, FORMATS, 
                       workspace_bytes, lib,
                       QF_STATE_BLOCK, QF_STATE_E4M3, QF_STATE_F32, PreparedStep, alloc_adamw_state,
                       alloc_grad_norm_workspace, prepare_adamw, prepare_grad_norm, qf_adamw,
-                      qf_grad_norm)
+                      qf_grad_norm, QF_LORA_APPLY_MAX_RANK, QF_LORA_MAX_ADAPTERS, alloc_lora_plan,
+                      alloc_lora_u, alloc_lora_workspace, lora_u_cols, prepare_lora_apply,
+                      prepare_lora_apply_backward, prepare_lora_plan, qf_lora_apply,
+                      qf_lora_apply_backward, qf_lora_plan)
 
 __all__ = ["QF_NVFP4", "QF_MXFP4", "QF_Q4K", "QF_X_BF16", "QF_X_F32", "FORMATS", "EXPORTS",
            "QfError", "alloc_outputs", "alloc_workspace", "output_sizes",
@@ -25,4 +28,7 @@ __all__ = ["QF_NVFP4", "QF_MXFP4", "QF_Q4K", "QF_X_BF16", "QF_X_F32", "FORMATS",
            "workspace_bytes", "lib",
            "QF_STATE_BLOCK", "QF_STATE_E4M3", "QF_STATE_F32", "PreparedStep", "alloc_adamw_state",
            "alloc_grad_norm_workspace", "prepare_adamw", "prepare_grad_norm", "qf_adamw",
-           "qf_grad_norm"]
+           "qf_grad_norm", "QF_LORA_APPLY_MAX_RANK", "QF_LORA_MAX_ADAPTERS", "alloc_lora_plan",
+           "alloc_lora_u", "alloc_lora_workspace", "lora_u_cols", "prepare_lora_apply",
+           "prepare_lora_apply_backward", "prepare_lora_plan", "qf_lora_apply",
+           "qf_lora_apply_backward", "qf_lora_plan"]

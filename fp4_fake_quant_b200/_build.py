@@ -9,7 +9,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqf.so")
-SOURCES = ["qf_api.cu", "qf_adamw.cu"]
+SOURCES = ["qf_api.cu", "qf_adamw.cu", "qf_adapters.cu"]
 HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith(".cuh"))   # every header counts
 
 NVCC_FLAGS = [

@@ -55,6 +55,18 @@ class QfAdamwOpt(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class QfLoraBatch(ctypes.Structure):
+    """Mirror of ``qf_lora_batch`` (include/qf.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("u", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("d_plan", ctypes.c_void_p)]
+
+
+class QfLoraGrad(ctypes.Structure):
+    """Mirror of ``qf_lora_grad`` (include/qf.h)."""
+    _fields_ = [("gb", ctypes.c_void_p), ("ga", ctypes.c_void_p)]
+
+
 class QfError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -91,7 +103,15 @@ def _load() -> ctypes.CDLL:
     lib.qf_grad_norm.argtypes = [Q, I, I, ctypes.c_double, P, P, P, ctypes.c_size_t, P]
     lib.qf_grad_norm_workspace_bytes.argtypes = []
     lib.qf_grad_norm_workspace_bytes.restype = ctypes.c_size_t
-    for f in (lib.qf_adamw, lib.qf_grad_norm, lib.qf_amax_tied, lib.qf_fakequant, lib.qf_pack, lib.qf_ste_backward,
+    S, B = ctypes.c_size_t, ctypes.POINTER(QfLoraBatch)
+    lib.qf_lora_plan.argtypes = [P, I64, I, P, S, P]
+    lib.qf_lora_plan_bytes.argtypes = [I64, I]
+    lib.qf_lora_plan_bytes.restype = S
+    lib.qf_lora_apply.argtypes = [L, I, B, P]
+    lib.qf_lora_apply_backward.argtypes = [L, ctypes.POINTER(QfLoraGrad), I, B, P, I64, P, I64, P, S, P]
+    lib.qf_lora_backward_workspace_bytes.argtypes = [L, I, I64, I64, I64]
+    lib.qf_lora_backward_workspace_bytes.restype = S
+    for f in (lib.qf_lora_plan, lib.qf_lora_apply, lib.qf_lora_apply_backward, lib.qf_adamw, lib.qf_grad_norm, lib.qf_amax_tied, lib.qf_fakequant, lib.qf_pack, lib.qf_ste_backward,
               lib.qf_lora_merge, lib.qf_amax_tied_lora, lib.qf_fakequant_lora,
               lib.qf_amax_fakequant, lib.qf_workspace_check, lib.qf_amax_fakequant_noalloc,
               lib.qf_amax_fakequant_lora, lib.qf_noalloc_check):
@@ -112,7 +132,9 @@ EXPORTS = ("qf_amax_tied", "qf_fakequant", "qf_pack", "qf_ste_backward", "qf_lor
            "qf_amax_tied_lora", "qf_fakequant_lora", "qf_amax_fakequant_lora",
            "qf_amax_fakequant", "qf_amax_fakequant_workspace_bytes", "qf_workspace_check",
            "qf_amax_fakequant_noalloc", "qf_noalloc_check", "qf_test_barrier_timeout",
-           "qf_adamw", "qf_grad_norm", "qf_grad_norm_workspace_bytes",
+           "qf_adamw", "qf_grad_norm", "qf_grad_norm_workspace_bytes", "qf_lora_plan",
+           "qf_lora_plan_bytes", "qf_lora_apply", "qf_lora_apply_backward",
+           "qf_lora_backward_workspace_bytes",
            "qf_status_string", "qf_last_error", "qf_version")
 
 
@@ -548,3 +570,146 @@ def qf_grad_norm(grads, norm, max_norm=0.0, step_tensor=None, workspace=None, st
     allocated for the call."""
     prepare_grad_norm(grads, norm, max_norm, step_tensor, workspace)(stream)
     return norm
+
+
+QF_LORA_APPLY_MAX_RANK, QF_LORA_MAX_ADAPTERS = 128, 512
+
+
+def _rows(what: str, t: torch.Tensor, tokens=None, width=None):
+    """(pointer, row stride) of a BF16 tensor seen as [tokens, width]: leading dimensions are
+    folded, the last one is dense, rows may be columns of a wider buffer."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be bfloat16")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libqf must be CUDA tensors")
+    if t.dim() < 2 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must have at least two dimensions and a dense last one")
+    if t.dim() > 2:
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{what}: the leading dimensions do not fold into one stride") from None
+    if (tokens is not None and t.shape[0] != tokens) or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, ({tokens}, {width}) expected")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0) // 8 * 8))
+
+
+def lora_u_cols(adapters) -> int:
+    """Columns of the u buffer: the largest rank, rounded up to a multiple of 16."""
+    return max((int(a.shape[0]) + 15) // 16 * 16 for _, a, _ in adapters)
+
+
+def alloc_lora_u(tokens: int, adapters) -> torch.Tensor:
+    """The u = x A^T buffer of one projection (a torch allocation; plumbing)."""
+    return torch.empty(tokens, lora_u_cols(adapters), dtype=torch.bfloat16, device=adapters[0][1].device)
+
+
+def alloc_lora_plan(tokens: int, n_adapters: int, device=None) -> torch.Tensor:
+    """Device memory for qf_lora_plan (a torch allocation; plumbing)."""
+    nbytes = int(lib.qf_lora_plan_bytes(int(tokens), int(n_adapters)))
+    if nbytes == 0:
+        raise ValueError(f"no plan for {tokens} tokens and {n_adapters} adapters")
+    return torch.empty(nbytes // 4, dtype=torch.int32,
+                       device=torch.device(device) if device is not None else torch.device("cuda"))
+
+
+def alloc_lora_workspace(tokens: int, adapters) -> torch.Tensor:
+    """Workspace of qf_lora_apply_backward for one projection's adapters (a torch allocation)."""
+    arr = _lora(adapters)
+    b, a, _ = adapters[0]
+    nbytes = int(lib.qf_lora_backward_workspace_bytes(arr, len(adapters), int(tokens), b.shape[0], a.shape[1]))
+    if nbytes == 0:
+        raise ValueError("no workspace for these sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=a.device)
+
+
+def prepare_lora_plan(index: torch.Tensor, n_adapters: int, plan: torch.Tensor) -> Prepared:
+    if index.dtype != torch.int32 or plan.dtype != torch.int32:
+        raise TypeError("index and plan must be int32")
+    _on_device("qf_lora_plan", [index, plan])
+    return Prepared(lib.qf_lora_plan, (_ptr(index), index.numel(), int(n_adapters), _ptr(plan),
+                                       plan.numel() * 4), (index, plan))
+
+
+def qf_lora_plan(index: torch.Tensor, n_adapters: int, plan: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Group a batch's tokens by adapter: ``index`` int32, one entry per token (negative: no
+    adapter).  One plan serves every projection of the batch."""
+    if plan is None:
+        plan = alloc_lora_plan(index.numel(), n_adapters, index.device)
+    prepare_lora_plan(index, n_adapters, plan)(stream)
+    return plan
+
+
+def _lora_batch(what, x, adapters, y, u, plan):
+    if not adapters:
+        raise ValueError(f"{what}: no adapters")
+    rows, cols = adapters[0][0].shape[0], adapters[0][1].shape[1]
+    for b, a, _ in adapters:
+        if b.dim() != 2 or a.dim() != 2 or b.shape[0] != rows or a.shape[1] != cols or b.shape[1] != a.shape[0]:
+            raise ValueError(f"{what}: adapters must be (b [{rows}, rank], a [rank, {cols}], scale)")
+    _on_device(what, [x, y, u, plan, *(t for b, a, _ in adapters for t in (b, a))])
+    tokens = x.numel() // max(x.shape[-1], 1)
+    c = QfLoraBatch(tokens=tokens, rows=rows, cols=cols)
+    c.x, c.ldx = _rows("x", x, tokens, cols)
+    if y is not None:
+        c.y, c.ldy = _rows("y", y, tokens, rows)
+    if u.dtype != torch.bfloat16 or tuple(u.shape) != (tokens, lora_u_cols(adapters)):
+        raise ValueError(f"u must be bfloat16 ({tokens}, {lora_u_cols(adapters)})")
+    c.u = _ptr(u)
+    if plan is not None:
+        if plan.dtype != torch.int32 or plan.numel() * 4 < int(lib.qf_lora_plan_bytes(tokens, len(adapters))):
+            raise ValueError("plan is too small for this batch")
+        c.d_plan = _ptr(plan)
+    return c, tokens, rows, cols
+
+
+def prepare_lora_apply(x, adapters, y, u, plan=None) -> Prepared:
+    c, *_ = _lora_batch("qf_lora_apply", x, adapters, y, u, plan)
+    la = _lora(adapters)
+    return Prepared(lib.qf_lora_apply, (la, len(adapters), ctypes.byref(c)),
+                    (la, c, x, list(adapters), y, u, plan))
+
+
+def qf_lora_apply(x, adapters, y, u=None, plan=None, stream=None) -> torch.Tensor:
+    """y += scale * (x a^T) b^T with each token's adapter ((b, a, scale) triples; ``plan`` from
+    qf_lora_plan, None: one adapter for every token).  ``y`` holds the shared projection's
+    output.  Returns u = x a^T, which the backward call reads."""
+    if u is None:
+        u = alloc_lora_u(x.numel() // max(x.shape[-1], 1), adapters)
+    prepare_lora_apply(x, adapters, y, u, plan)(stream)
+    return u
+
+
+def prepare_lora_apply_backward(x, gy, adapters, u, gx=None, ga=None, gb=None, plan=None,
+                                workspace=None) -> Prepared:
+    c, tokens, rows, cols = _lora_batch("qf_lora_apply_backward", x, adapters, None, u, plan)
+    if (ga is None) != (gb is None):
+        raise ValueError("ga and gb come together")
+    if workspace is None:
+        workspace = alloc_lora_workspace(tokens, adapters)
+    _on_device("qf_lora_apply_backward", [x, gy, gx, workspace, *(ga or ()), *(gb or ())])
+    py, ldgy = _rows("gy", gy, tokens, rows)
+    px, ldgx = _rows("gx", gx, tokens, cols) if gx is not None else (None, 0)
+    grads = None
+    if ga is not None:
+        grads = (QfLoraGrad * len(adapters))()
+        if len(ga) != len(adapters) or len(gb) != len(adapters):
+            raise ValueError("one ga and one gb per adapter")
+        for d, wa, wb, (b, a, _) in zip(grads, ga, gb, adapters):
+            if wa.dtype != torch.bfloat16 or wb.dtype != torch.bfloat16 or wa.shape != a.shape or wb.shape != b.shape:
+                raise ValueError("ga and gb must be bfloat16 and shaped like their factors")
+            d.ga, d.gb = _ptr(wa), _ptr(wb)
+    la = _lora(adapters)
+    return Prepared(lib.qf_lora_apply_backward,
+                    (la, grads, len(adapters), ctypes.byref(c), py, ldgy, px, ldgx, _ptr(workspace),
+                     workspace.numel() * workspace.element_size()),
+                    (la, grads, c, x, gy, list(adapters), u, gx, ga, gb, plan, workspace))
+
+
+def qf_lora_apply_backward(x, gy, adapters, u, gx=None, ga=None, gb=None, plan=None, workspace=None,
+                           stream=None) -> None:
+    """gx += scale * (gy b) a; ga[i], gb[i] <- the gradients of adapter i's factors (zero
+    without tokens).  ``gx`` holds the shared projection's own input gradient.  ``gx`` or
+    the pair ``ga``/``gb`` may be left out."""
+    prepare_lora_apply_backward(x, gy, adapters, u, gx, ga, gb, plan, workspace)(stream)

@@ -1,0 +1,349 @@
+// qf_adapters.cu -- entry points of the low-rank adapters of many requests beside a shared
+// projection: qf_lora_plan, qf_lora_apply, qf_lora_apply_backward (declared in
+// include/qf.h).  Host-side argument validation, descriptor tables, launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qf.h"
+#include "qf_adapters.cuh"
+#include "qf_host.cuh"
+
+namespace {
+
+using namespace qf_host;
+using qf::Adapter;
+using qf::AdapterTable;
+using qf::PlanView;
+using qf::kLoraMaxAdapters;
+using qf::kLoraMaxRank;
+using qf::kLoraThreads;
+using qf::kLoraTile;
+
+constexpr int kSmallA = 16, kLargeA = kLoraMaxAdapters;    // descriptor table sizes
+constexpr int64_t kMaxTokens = int64_t(1) << 26, kMaxWidth = int64_t(1) << 24;
+
+static_assert(QF_LORA_APPLY_MAX_RANK == kLoraMaxRank && QF_LORA_MAX_ADAPTERS == kLoraMaxAdapters, "");
+
+int round16(int r) { return (r + 15) / 16 * 16; }
+
+// A [tokens, width] BF16 matrix with row stride ld.
+struct Mat { const void* p; int64_t ld; int64_t width; };
+
+qf_status check_mat(const Mat& m, int64_t tokens, const char* name) {
+    if (m.p == nullptr) return fail(QF_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned16(m.p)) return fail(QF_ERR_ALIGN, "%s not 16-byte aligned", name);
+    if (m.ld % 8 != 0 || m.ld < m.width || m.ld > INT64_MAX / 4 / std::max<int64_t>(tokens, 1))
+        return fail(QF_ERR_SHAPE, "%s: row stride %lld (>= %lld and a multiple of 8 needed)", name,
+                    (long long)m.ld, (long long)m.width);
+    return QF_OK;
+}
+
+// Whether two matrices share memory; columns of one buffer side by side do not.
+bool share(const Mat& a, const Mat& b, int64_t tokens) {
+    const int64_t na = 2 * ((tokens - 1) * a.ld + a.width), nb = 2 * ((tokens - 1) * b.ld + b.width);
+    if (!overlap(a.p, na, b.p, nb)) return false;
+    if (a.ld != b.ld) return true;
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) / 2;
+    const int64_t off = ((d % a.ld) + a.ld) % a.ld;
+    return off < a.width || off + b.width > a.ld;
+}
+
+qf_status check_batch(const qf_lora* l, int n, const qf_lora_batch& c, int* max_rank) {
+    if (n < 1 || n > kLoraMaxAdapters)
+        return fail(QF_ERR_INVALID_ARG, "n = %d adapters outside [1, %d]", n, kLoraMaxAdapters);
+    if (l == nullptr) return fail(QF_ERR_INVALID_ARG, "adapter array is NULL");
+    if (c.tokens < 0 || c.rows < 0 || c.cols < 0) return fail(QF_ERR_SHAPE, "negative size");
+    if (c.tokens > kMaxTokens || c.rows > kMaxWidth || c.cols > kMaxWidth)
+        return fail(QF_ERR_SHAPE, "tokens above 2^26, or rows or cols above 2^24");
+    if (c.rows % 8 != 0 || c.cols % 8 != 0)
+        return fail(QF_ERR_SHAPE, "rows = %lld and cols = %lld must be multiples of 8",
+                    (long long)c.rows, (long long)c.cols);
+    if (c.d_plan == nullptr && n != 1)
+        return fail(QF_ERR_INVALID_ARG, "without a plan there is one adapter, not %d", n);
+    if ((reinterpret_cast<uintptr_t>(c.d_plan) & 3) != 0) return fail(QF_ERR_ALIGN, "plan not 4-byte aligned");
+    *max_rank = 0;
+    for (int i = 0; i < n; ++i) {
+        if (l[i].rank < 1 || l[i].rank > kLoraMaxRank)
+            return fail(QF_ERR_INVALID_ARG, "adapter %d: rank %d outside [1, %d]", i, (int)l[i].rank, kLoraMaxRank);
+        if ((c.rows > 0 && l[i].b == nullptr) || (c.cols > 0 && l[i].a == nullptr))
+            return fail(QF_ERR_INVALID_ARG, "adapter %d: a or b is NULL", i);
+        if (!aligned16(l[i].a) || (reinterpret_cast<uintptr_t>(l[i].b) & 1) != 0)
+            return fail(QF_ERR_ALIGN, "adapter %d: a not 16-byte or b not 2-byte aligned", i);
+        *max_rank = std::max(*max_rank, (int)l[i].rank);
+    }
+    return QF_OK;
+}
+
+qf_status check_u(const qf_lora_batch& c) {
+    if (c.u == nullptr) return fail(QF_ERR_INVALID_ARG, "u is NULL");
+    if (!aligned16(c.u)) return fail(QF_ERR_ALIGN, "u not 16-byte aligned");
+    return QF_OK;
+}
+
+// One launch, optionally as a programmatic dependent of the kernel before it (each kernel
+// here waits for that one's results first) and in clusters.
+template <typename K, typename... Args>
+qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, bool dependent,
+                 dim3 cluster, Args... args) {
+    Shape shape;                                   // (also raises the shared-memory limit once)
+    const qf_status st = shape_of(kernel, threads, smem, &shape);
+    if (st != QF_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int k = 0;
+    if (dependent) {
+        attr[k].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[k++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster.x * cluster.y * cluster.z > 1) {
+        attr[k].id = cudaLaunchAttributeClusterDimension;
+        attr[k].val.clusterDim.x = cluster.x;
+        attr[k].val.clusterDim.y = cluster.y;
+        attr[k++].val.clusterDim.z = cluster.z;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = k;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? QF_OK : cuda_fail(e, "cudaLaunchKernelEx");
+}
+
+#ifndef QF_LORA_CTAS
+#define QF_LORA_CTAS 592        // CTAs the split of a reduction aims at (4 per SM)
+#endif
+// Cluster size: how many CTAs share one reduction, so that `units` of them fill the GPU;
+// at most 8 (portable) and at most one per `steps` of work.
+int parts_for(int64_t units, int64_t steps) {
+    int p = 1;
+    while (p < 8 && units * p < QF_LORA_CTAS && 2 * p <= steps) p *= 2;
+    return p;
+}
+
+template <int NT> constexpr size_t down_smem() {
+    return size_t(NT > 4 ? 4 : 8) * kLoraTile * (NT * 8 + 4) * sizeof(float);
+}
+
+template <int MAXA, int NT>
+qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
+               int64_t depth, bool backward, void* u, int ldu, bool dependent, cudaStream_t s) {
+    const int parts = parts_for(tiles, (depth + 255) / 256);
+    if (tiles * parts > INT32_MAX) return fail(QF_ERR_SHAPE, "too many tokens for one launch");
+    return launch(qf::k_lora_down<MAXA, NT>, dim3((unsigned)(tiles * parts)), kLoraThreads, down_smem<NT>(), s,
+                  dependent, dim3(parts), A, P, static_cast<const uint16_t*>(z), ldz, (int)depth,
+                  (int)backward, parts, static_cast<uint16_t*>(u), ldu);
+}
+template <int MAXA>
+qf_status down_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
+                   int64_t depth, bool backward, void* u, int ldu, bool dependent, cudaStream_t s) {
+    if (ldu <= 16) return down<MAXA, 2>(A, P, tiles, z, ldz, depth, backward, u, ldu, dependent, s);
+    if (ldu <= 32) return down<MAXA, 4>(A, P, tiles, z, ldz, depth, backward, u, ldu, dependent, s);
+    return down<MAXA, 8>(A, P, tiles, z, ldz, depth, backward, u, ldu, dependent, s);
+}
+
+template <int MAXA, int KS>
+qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int ldu,
+             int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
+    const int64_t blocks = tiles * ((width + 255) / 256);
+    if (blocks > INT32_MAX) return fail(QF_ERR_SHAPE, "tokens x width too large for one launch");
+    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), kLoraThreads, 0, s, true, dim3(1), A, P,
+                  static_cast<const uint16_t*>(u), ldu, (int)width, (int)backward,
+                  static_cast<uint16_t*>(y), ldy);
+}
+template <int MAXA>
+qf_status up_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int ldu,
+                 int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
+    if (ldu <= 16) return up<MAXA, 1>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
+    if (ldu <= 32) return up<MAXA, 2>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
+    if (ldu <= 64) return up<MAXA, 4>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
+    return up<MAXA, 8>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
+}
+
+template <int MAXA, int MT>
+qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf_lora_batch& c, const void* v,
+                const void* gy, int64_t ldgy, int ldu, cudaStream_t s) {
+    const int64_t tiles = (c.cols + qf::kGradCols - 1) / qf::kGradCols + (c.rows + qf::kGradCols - 1) / qf::kGradCols;
+    const int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens);
+    return launch(qf::k_lora_grad<MAXA, MT>, dim3((unsigned)tiles, n, parts), qf::kGradThreads,
+                  qf::grad_smem<MT>(), s, true, dim3(1, 1, parts), G, P, static_cast<const uint16_t*>(c.x),
+                  c.ldx, (int)c.cols, static_cast<const uint16_t*>(v), static_cast<const uint16_t*>(gy), ldgy,
+                  (int)c.rows, static_cast<const uint16_t*>(c.u), ldu);
+}
+
+template <int MAXA>
+void fill(AdapterTable<MAXA>& A, const qf_lora* l, int n) {
+    for (int i = 0; i < n; ++i)
+        A.t[i] = Adapter{static_cast<const uint16_t*>(l[i].b), static_cast<const uint16_t*>(l[i].a),
+                         (int)l[i].rank, l[i].scale};
+}
+
+PlanView plan_view(const qf_lora_batch& c, int n) {
+    return PlanView{static_cast<const int32_t*>(c.d_plan), (int)c.tokens, n};
+}
+int64_t tiles_of(const qf_lora_batch& c, int n) {
+    return c.d_plan ? qf::plan_tiles(c.tokens, n) : (c.tokens + kLoraTile - 1) / kLoraTile;
+}
+
+template <int MAXA>
+qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int ldu, cudaStream_t s) {
+    AdapterTable<MAXA> A;
+    fill(A, l, n);
+    const PlanView P = plan_view(c, n);
+    const int64_t tiles = tiles_of(c, n);
+    qf_status st = down_any<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, ldu, false, s);
+    if (st != QF_OK || c.rows == 0) return st;
+    return up_any<MAXA>(A, P, tiles, c.u, ldu, c.rows, false, c.y, c.ldy, s);
+}
+
+int64_t aligned(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+template <int MAXA>
+qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora_batch& c, const void* gy,
+                   int64_t ldgy, void* gx, int64_t ldgx, void* ws, int ldu, cudaStream_t s) {
+    qf::TurnTable<MAXA> T;
+    AdapterTable<MAXA> A;
+    fill(A, l, n);
+    char* at = static_cast<char*>(ws);
+    uint16_t* const v = reinterpret_cast<uint16_t*>(at);
+    at += aligned(2 * c.tokens * ldu);
+    int wide = 0;
+    for (int i = 0; i < n; ++i) {
+        T.t[i] = A.t[i];
+        T.at[i] = reinterpret_cast<uint16_t*>(at);
+        at += aligned(2 * c.cols * round16(l[i].rank));
+        T.bt[i] = reinterpret_cast<uint16_t*>(at);
+        at += aligned(2 * c.rows * l[i].rank);
+        wide = std::max(wide, round16(l[i].rank));
+    }
+    const int64_t work = (c.cols + c.rows) * (wide / 8);
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((work + 255) / 256, 1024));
+    qf_status st = launch(qf::k_lora_turn<MAXA>, dim3((unsigned)blocks, n), 256, 0, s, false, dim3(1), T,
+                          (int)c.rows, (int)c.cols);
+    if (st != QF_OK) return st;
+    for (int i = 0; i < n; ++i) {
+        A.t[i].a = T.at[i];
+        A.t[i].b = T.bt[i];
+    }
+    const PlanView P = plan_view(c, n);
+    const int64_t tiles = tiles_of(c, n);
+    if (c.tokens > 0) {
+        st = down_any<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, ldu, true, s);
+        if (st != QF_OK) return st;
+        if (gx && c.cols > 0) {
+            st = up_any<MAXA>(A, P, tiles, v, ldu, c.cols, true, gx, ldgx, s);
+            if (st != QF_OK) return st;
+        }
+    }
+    if (!g || c.cols + c.rows == 0) return QF_OK;
+    qf::GradTable<MAXA> G;
+    for (int i = 0; i < n; ++i) {
+        G.t[i] = qf::GradOut{g[i].ga, g[i].gb};
+        G.scale[i] = l[i].scale;
+        G.rank[i] = l[i].rank;
+    }
+    if (ldu <= 16) return grads<MAXA, 1>(G, P, n, c, v, gy, ldgy, ldu, s);
+    if (ldu <= 32) return grads<MAXA, 2>(G, P, n, c, v, gy, ldgy, ldu, s);
+    if (ldu <= 64) return grads<MAXA, 4>(G, P, n, c, v, gy, ldgy, ldu, s);
+    return grads<MAXA, 8>(G, P, n, c, v, gy, ldgy, ldu, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qf_lora_plan_bytes(int64_t tokens, int n_adapters) {
+    if (tokens < 0 || tokens > kMaxTokens || n_adapters < 1 || n_adapters > kLoraMaxAdapters) return 0;
+    return sizeof(int32_t) * (size_t)qf::plan_words(tokens, n_adapters);
+}
+
+qf_status qf_lora_plan(const int32_t* d_index, int64_t tokens, int n_adapters, void* d_plan,
+                       size_t plan_bytes, void* stream) {
+    g_err[0] = 0;
+    if (n_adapters < 1 || n_adapters > kLoraMaxAdapters)
+        return fail(QF_ERR_INVALID_ARG, "n_adapters = %d outside [1, %d]", n_adapters, kLoraMaxAdapters);
+    if (tokens < 0 || tokens > kMaxTokens)
+        return fail(QF_ERR_SHAPE, "tokens = %lld outside [0, 2^26]", (long long)tokens);
+    if (tokens > 0 && d_index == nullptr) return fail(QF_ERR_INVALID_ARG, "d_index is NULL");
+    if (d_plan == nullptr || plan_bytes < qf_lora_plan_bytes(tokens, n_adapters))
+        return fail(QF_ERR_INVALID_ARG, "plan of %zu bytes, %zu needed", d_plan ? plan_bytes : (size_t)0,
+                    qf_lora_plan_bytes(tokens, n_adapters));
+    if (((reinterpret_cast<uintptr_t>(d_index) | reinterpret_cast<uintptr_t>(d_plan)) & 3) != 0)
+        return fail(QF_ERR_ALIGN, "d_index or d_plan not 4-byte aligned");
+    if (overlap(d_index, 4 * tokens, d_plan, (int64_t)plan_bytes))
+        return fail(QF_ERR_INVALID_ARG, "d_index and d_plan overlap");
+    qf::k_lora_plan<<<n_adapters, qf::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        d_index, (int)tokens, n_adapters, static_cast<int32_t*>(d_plan));
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? QF_OK : cuda_fail(e, "kernel launch");
+}
+
+qf_status qf_lora_apply(const qf_lora* l, int n, const qf_lora_batch* batch, void* stream) {
+    g_err[0] = 0;
+    if (batch == nullptr) return fail(QF_ERR_INVALID_ARG, "batch is NULL");
+    const qf_lora_batch& c = *batch;
+    int max_rank = 0;
+    qf_status st = check_batch(l, n, c, &max_rank);
+    if (st != QF_OK || c.tokens == 0) return st;
+    const Mat x{c.x, c.ldx, c.cols}, y{c.y, c.ldy, c.rows}, u{c.u, round16(max_rank), round16(max_rank)};
+    if (c.cols > 0 && (st = check_mat(x, c.tokens, "x")) != QF_OK) return st;
+    if (c.rows > 0 && (st = check_mat(y, c.tokens, "y")) != QF_OK) return st;
+    if ((st = check_u(c)) != QF_OK) return st;
+    if (share(x, y, c.tokens) || share(x, u, c.tokens) || share(y, u, c.tokens))
+        return fail(QF_ERR_INVALID_ARG, "x, y and u must not overlap");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return n <= kSmallA ? apply<kSmallA>(l, n, c, round16(max_rank), s)
+                        : apply<kLargeA>(l, n, c, round16(max_rank), s);
+}
+
+size_t qf_lora_backward_workspace_bytes(const qf_lora* l, int n, int64_t tokens, int64_t rows, int64_t cols) {
+    if (l == nullptr || n < 1 || n > kLoraMaxAdapters || tokens < 0 || rows < 0 || cols < 0 ||
+        tokens > kMaxTokens || rows > kMaxWidth || cols > kMaxWidth)
+        return 0;
+    int max_rank = 0;
+    int64_t bytes = 0;
+    for (int i = 0; i < n; ++i) {
+        if (l[i].rank < 1 || l[i].rank > kLoraMaxRank) return 0;
+        max_rank = std::max(max_rank, (int)l[i].rank);
+        bytes += aligned(2 * cols * round16(l[i].rank)) + aligned(2 * rows * l[i].rank);
+    }
+    return (size_t)(bytes + aligned(2 * tokens * round16(max_rank)));
+}
+
+qf_status qf_lora_apply_backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora_batch* batch,
+                                 const void* gy, int64_t ldgy, void* gx, int64_t ldgx, void* d_workspace,
+                                 size_t workspace_bytes, void* stream) {
+    g_err[0] = 0;
+    if (batch == nullptr) return fail(QF_ERR_INVALID_ARG, "batch is NULL");
+    const qf_lora_batch& c = *batch;
+    int max_rank = 0;
+    qf_status st = check_batch(l, n, c, &max_rank);
+    if (st != QF_OK) return st;
+    if (gx == nullptr && g == nullptr) return fail(QF_ERR_INVALID_ARG, "no output: gx and g are NULL");
+    const int ldu = round16(max_rank);
+    const Mat x{c.x, c.ldx, c.cols}, u{c.u, ldu, ldu}, my{gy, ldgy, c.rows}, mx{gx, ldgx, c.cols};
+    if (c.tokens > 0) {
+        if (c.rows > 0 && (st = check_mat(my, c.tokens, "gy")) != QF_OK) return st;
+        if (gx && c.cols > 0 && (st = check_mat(mx, c.tokens, "gx")) != QF_OK) return st;
+        if (g && c.cols > 0 && (st = check_mat(x, c.tokens, "x")) != QF_OK) return st;
+        if (g && (st = check_u(c)) != QF_OK) return st;
+        if (gx && (share(mx, my, c.tokens) || (g && (share(mx, x, c.tokens) || share(mx, u, c.tokens)))))
+            return fail(QF_ERR_INVALID_ARG, "gx must not overlap gy, x or u");
+    }
+    for (int i = 0; g && i < n; ++i)
+        if ((c.cols > 0 && g[i].ga == nullptr) || (c.rows > 0 && g[i].gb == nullptr) ||
+            ((reinterpret_cast<uintptr_t>(g[i].ga) | reinterpret_cast<uintptr_t>(g[i].gb)) & 1) != 0)
+            return fail(QF_ERR_INVALID_ARG, "adapter %d: ga or gb is NULL or not 2-byte aligned", i);
+    const size_t need = qf_lora_backward_workspace_bytes(l, n, c.tokens, c.rows, c.cols);
+    if (d_workspace == nullptr || workspace_bytes < need)
+        return fail(QF_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed",
+                    d_workspace ? workspace_bytes : (size_t)0, need);
+    if (!aligned16(d_workspace)) return fail(QF_ERR_ALIGN, "workspace not 16-byte aligned");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return n <= kSmallA ? backward<kSmallA>(l, g, n, c, gy, ldgy, gx, ldgx, d_workspace, ldu, s)
+                        : backward<kLargeA>(l, g, n, c, gy, ldgy, gx, ldgx, d_workspace, ldu, s);
+}
+
+}  // extern "C"

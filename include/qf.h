@@ -498,6 +498,100 @@ qf_status qf_grad_norm(const qf_param* t, int n, int g_type, double max_norm, fl
                        int64_t* d_step, void* d_workspace, size_t workspace_bytes, void* stream);
 size_t qf_grad_norm_workspace_bytes(void);
 
+/*
+ * Low-rank adapters beside a shared projection.  qf_lora_merge and its kin fold ONE adapter
+ * into a weight; these calls leave the shared weight alone and add each token's own adapter
+ * to the projection's output, for a batch whose requests have different adapters (serving
+ * before the merge, evaluation of several adapters, LoRA-QAD training of one or more on a
+ * quantized base: project page, Method, "QAD").
+ *
+ * With adapter i = l[index[t]] of token t (b [rows, rank], a [rank, cols], scale; BF16,
+ * a 16-byte aligned; rank 1 .. QF_LORA_APPLY_MAX_RANK, the adapters' ranks may differ):
+ *   u[t] = BF16( sum over c of x[t,c] a[k,c] ),  k < rank
+ *   y[t] = BF16( y[t] + scale * sum over k of u[t,k] b[r,k] ),  r < rows
+ * Sums in FP32 on the tensor cores, in an order that is fixed for a device, so equal calls
+ * give equal bits.  A token without an adapter is left as it was (y, u, gx).
+ */
+#define QF_LORA_APPLY_MAX_RANK 128
+#define QF_LORA_MAX_ADAPTERS 512
+
+/*
+ * qf_lora_plan -- groups a batch's tokens by adapter, on the device; made once per batch and
+ * used by every projection's calls.
+ *   d_index   DEVICE int32[tokens]: each token's adapter in [0, n_adapters); any other value
+ *             (e.g. -1): none.  In any order: a request's tokens need not be neighbours.
+ *   tokens    0 .. 2^26;  n_adapters  1 .. QF_LORA_MAX_ADAPTERS
+ *   d_plan    DEVICE memory of qf_lora_plan_bytes(tokens, n_adapters) bytes, 4-byte aligned,
+ *             overwritten.
+ */
+qf_status qf_lora_plan(const int32_t* d_index, int64_t tokens, int n_adapters, void* d_plan,
+                       size_t plan_bytes, void* stream);
+size_t qf_lora_plan_bytes(int64_t tokens, int n_adapters);     /* 0 for sizes out of range */
+
+/*
+ * One projection's batch.
+ *   x       BF16 [tokens, cols], row stride ldx elements: the projection's input
+ *   y       BF16 [tokens, rows], row stride ldy: the shared projection's output, added to
+ *           in place (qf_lora_apply only)
+ *   u       BF16 [tokens, R], contiguous, R = the largest rank rounded up to a multiple of
+ *           16: written by qf_lora_apply (each token's columns up to its adapter's rank, and
+ *           zeros up to the next multiple of 16), read by qf_lora_apply_backward
+ *   rows, cols   multiples of 8, at most 2^24
+ *   d_plan  from qf_lora_plan for the same tokens and number of adapters (for other sizes
+ *           the call leaves its outputs as they were), or NULL: one adapter, every token
+ * x, y and u are 16-byte aligned, strides multiples of 8 (columns of one wider buffer are
+ * fine), and x, y, u do not overlap.
+ */
+typedef struct qf_lora_batch {
+    const void* x;
+    int64_t ldx;
+    void* y;
+    int64_t ldy;
+    void* u;
+    int64_t tokens;
+    int64_t rows;
+    int64_t cols;
+    const void* d_plan;
+} qf_lora_batch;
+
+/*
+ * qf_lora_apply -- the forward pass above for n adapters (n >= 1; without a plan n == 1).
+ * Errors: n out of range, a NULL pointer, a rank out of range, overlapping buffers ->
+ *   QF_ERR_INVALID_ARG; a size or stride out of range -> QF_ERR_SHAPE; QF_ERR_ALIGN.
+ */
+qf_status qf_lora_apply(const qf_lora* l, int n, const qf_lora_batch* batch, void* stream);
+
+/* One adapter's gradients: ga BF16 [rank, cols], gb BF16 [rows, rank], overwritten (zero for
+ * an adapter without tokens). */
+typedef struct qf_lora_grad {
+    void* gb;
+    void* ga;
+} qf_lora_grad;
+
+/*
+ * qf_lora_apply_backward -- with gy the gradient of y:
+ *   v[t]   = BF16( sum over r of gy[t,r] b[r,k] )
+ *   gx[t]  = BF16( gx[t] + scale * sum over k of v[t,k] a[k,c] )
+ *   ga     = BF16( scale * sum over the adapter's tokens of v[t,k] x[t,c] )
+ *   gb     = BF16( scale * sum over the adapter's tokens of gy[t,r] u[t,k] )
+ * (the gradient of y through the shared projection's input side is the caller's: gx holds
+ * it before the call.)
+ *   g       n entries, or NULL: no gradients of the factors (x and u are then not read)
+ *   gy      BF16 [tokens, rows], row stride ldgy
+ *   gx      BF16 [tokens, cols], row stride ldgx, added to in place, or NULL: not wanted
+ *   batch   x, u, sizes and plan as in the forward call; y is ignored
+ *   d_workspace  DEVICE memory of qf_lora_backward_workspace_bytes(...) bytes, 16-byte
+ *           aligned; its contents need not be kept.  Calls that may overlap need their own.
+ * Errors as for qf_lora_apply; neither gx nor g -> QF_ERR_INVALID_ARG.
+ */
+qf_status qf_lora_apply_backward(const qf_lora* l, const qf_lora_grad* g, int n,
+                                 const qf_lora_batch* batch, const void* gy, int64_t ldgy, void* gx,
+                                 int64_t ldgx, void* d_workspace, size_t workspace_bytes,
+                                 void* stream);
+/* Workspace of qf_lora_apply_backward (only l[i].rank is read); 0 for sizes out of range. */
+size_t qf_lora_backward_workspace_bytes(const qf_lora* l, int n, int64_t tokens, int64_t rows,
+                                        int64_t cols);
+
 /* Static description of a status code. */
 const char* qf_status_string(qf_status s);
 
@@ -509,7 +603,8 @@ const char* qf_last_error(void);
  * 1.3 QF_Q4K_MSE; 1.4 qf_amax_fakequant, its workspace calls and QF_ERR_TIMEOUT;
  * 1.5 qf_amax_fakequant_noalloc; 1.6 qf_amax_fakequant_lora; 1.7 sticky workspace
  * error flags, qf_noalloc_check and qf_test_barrier_timeout.  Calls added since only add
- * symbols (qf_adamw, qf_grad_norm); nothing that 1.7 declares changed. */
+ * symbols (qf_adamw, qf_grad_norm, qf_lora_plan, qf_lora_apply, qf_lora_apply_backward);
+ * nothing that 1.7 declares changed. */
 int qf_version(void);
 
 #ifdef __cplusplus

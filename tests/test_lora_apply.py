@@ -1,0 +1,464 @@
+"""qf_lora_plan, qf_lora_apply and qf_lora_apply_backward: refusals on the host; on the GPU,
+closeness to the formulas in 64 bits at the sizes, ranks, orders and strides where they can
+go wrong, gradients against differences, rows without an adapter, graphs and streams.
+
+Tolerances count roundings: u and v are rounded to BF16 (half a step, 2^-8 relative), outputs
+too; FP32 sums of n products on the tensor cores are within (n / 16 + 64) 2^-23 of the sum of
+their magnitudes (one addition per MMA, sixteen products inside one, and up to 64 partial
+sums joined)."""
+import ctypes
+
+import pytest
+import torch
+
+import fp4_fake_quant_b200 as qf
+
+DEV = "cuda:0"
+H = 2.0 ** -8                      # half a BF16 step, relative
+
+
+# ------------------------------------------------------------------ host refusals
+
+def _l(n=1, b=0x10000, a=0x20000, rank=16, scale=1.0):
+    arr = (qf.binding.QfLora * max(n, 1))()
+    for t in arr:
+        t.b, t.a, t.rank, t.scale = b, a, rank, scale
+    return arr
+
+
+def _batch(**over):
+    c = qf.binding.QfLoraBatch(x=0x1000000, ldx=64, y=0x2000000, ldy=32, u=0x3000000, tokens=10,
+                               rows=32, cols=64, d_plan=0x4000000)
+    for k, v in over.items():
+        setattr(c, k, v)
+    return c
+
+
+BAD = [
+    (1, _l(), 0, {}), (1, _l(), 513, {}), (1, None, 1, {}),
+    (1, _l(rank=0), 1, {}), (1, _l(rank=129), 1, {}), (1, _l(b=0), 1, {}), (1, _l(a=0), 1, {}),
+    (3, _l(a=0x20008), 1, {}), (3, _l(b=0x10001), 1, {}),
+    (1, _l(2), 2, {"d_plan": 0}), (3, _l(), 1, {"d_plan": 0x4000002}),
+    (2, _l(), 1, {"tokens": -1}), (2, _l(), 1, {"tokens": (1 << 26) + 1}),
+    (2, _l(), 1, {"rows": 12}), (2, _l(), 1, {"cols": 60}), (2, _l(), 1, {"cols": -8}),
+    (2, _l(), 1, {"rows": (1 << 24) + 8}),
+]
+
+
+@pytest.mark.parametrize("status,l,n,over", BAD + [
+    (1, _l(), 1, {"x": 0}), (1, _l(), 1, {"y": 0}), (1, _l(), 1, {"u": 0}),
+    (3, _l(), 1, {"x": 0x1000008}), (3, _l(), 1, {"y": 0x2000002}), (3, _l(), 1, {"u": 0x3000004}),
+    (2, _l(), 1, {"ldx": 56}), (2, _l(), 1, {"ldx": 68}), (2, _l(), 1, {"ldy": 36}),
+    (1, _l(), 1, {"y": 0x1000010}), (1, _l(), 1, {"u": 0x2000000}),
+])
+def test_apply_refusals(status, l, n, over):
+    assert qf.lib.qf_lora_apply(l, n, ctypes.byref(_batch(**over)), None) == status
+    assert qf.lib.qf_last_error()
+
+
+def _back(l=_l(), g=True, n=1, gy=0x5000000, ldgy=32, gx=0x6000000, ldgx=64, ws=0x8000000, wb=1 << 20, **over):
+    grads = (qf.binding.QfLoraGrad * 1)()
+    grads[0].ga, grads[0].gb = (0x7000000, 0x7100000) if g is True else g or (0, 0)
+    return qf.lib.qf_lora_apply_backward(l, grads if g else None, n, ctypes.byref(_batch(**over)), gy, ldgy,
+                                         gx, ldgx, ws, wb, None)
+
+
+@pytest.mark.parametrize("status,l,n,over", BAD)
+def test_backward_refuses_what_forward_does(status, l, n, over):
+    assert _back(l=l, n=n, **over) == status
+
+
+def test_backward_refusals():
+    assert _back(gx=None, g=None) == 1
+    assert _back(gy=None) == 1 and _back(gy=0x5000002) == 3 and _back(ldgy=24) == 2
+    assert _back(gx=0x6000004) == 3 and _back(ldgx=60) == 2
+    assert _back(g=(0, 0x7100000)) == 1 and _back(g=(0x7000000, 0)) == 1 and _back(g=(0x7000001, 0x7100000)) == 1
+    assert _back(ws=None) == 1 and _back(ws=0x8000004) == 3
+    need = qf.lib.qf_lora_backward_workspace_bytes(_l(), 1, 10, 32, 64)
+    assert need > 0 and _back(wb=need - 1) == 1
+    assert _back(gx=0x5000010) == 1 and _back(gx=0x1000000) == 1            # over gy, over x
+    assert qf.lib.qf_lora_backward_workspace_bytes(_l(rank=200), 1, 10, 32, 64) == 0
+    assert qf.lib.qf_lora_apply_backward(_l(), None, 1, None, 0, 0, 0, 0, 0, 0, None) == 1
+
+
+def test_columns_of_one_buffer_do_not_overlap():
+    """x and y side by side in one buffer pass the checks (the call then fails for want of a
+    GPU, or of that memory); x and y that share a column do not."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present (the pointers are fake)")
+    side = dict(x=0x1000000, ldx=96, ldy=96)
+    assert qf.lib.qf_lora_apply(_l(), 1, ctypes.byref(_batch(y=0x1000000 + 128, **side)), None) == 5
+    assert qf.lib.qf_lora_apply(_l(), 1, ctypes.byref(_batch(y=0x1000000 + 112, **side)), None) == 1
+
+
+def test_plan_refusals_and_sizes():
+    call, size = qf.lib.qf_lora_plan, qf.lib.qf_lora_plan_bytes
+    need = size(100, 3)
+    assert need == 4 * (4 + 4 + 100 + 2 * (2 + 3))
+    assert size(-1, 3) == 0 and size(100, 0) == 0 and size(100, 513) == 0 and size((1 << 26) + 1, 1) == 0
+    assert call(0x1000, 100, 0, 0x9000, need, None) == 1 and call(0x1000, 100, 513, 0x9000, need, None) == 1
+    assert call(0x1000, -1, 3, 0x9000, need, None) == 2 and call(None, 100, 3, 0x9000, need, None) == 1
+    assert call(0x1000, 100, 3, None, need, None) == 1 and call(0x1000, 100, 3, 0x9000, need - 1, None) == 1
+    assert call(0x1002, 100, 3, 0x9000, need, None) == 3 and call(0x1000, 100, 3, 0x1010, need, None) == 1
+
+
+def test_struct_layouts_match_the_header():
+    assert ctypes.sizeof(qf.binding.QfLoraBatch) == 72 and ctypes.sizeof(qf.binding.QfLoraGrad) == 16
+
+
+def test_nothing_to_do():
+    assert qf.lib.qf_lora_apply(_l(), 1, ctypes.byref(_batch(tokens=0, x=0, y=0, u=0)), None) == 0
+
+
+def test_binding_refusals():
+    x, y = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16)
+    ad = [(torch.zeros(8, 2, dtype=torch.bfloat16), torch.zeros(2, 16, dtype=torch.bfloat16), 1.0)]
+    u = torch.zeros(4, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):                               # not on a GPU
+        qf.qf_lora_apply(x, ad, y, u)
+    with pytest.raises(ValueError):
+        qf.qf_lora_apply(x, [], y, u)
+    with pytest.raises(ValueError):                               # factors that do not fit
+        qf.qf_lora_apply(x, [(ad[0][0], ad[0][1][:, :8], 1.0), ad[0]], y, u)
+    with pytest.raises(TypeError):
+        qf.qf_lora_plan(torch.zeros(4, dtype=torch.int64), 1, torch.zeros(64, dtype=torch.int32))
+    assert qf.lora_u_cols(ad) == 16
+
+
+# ------------------------------------------------------------------ the batch and its reference
+
+class Batch:
+    """Inputs of one projection on the device, and the formulas in 64 bits on the host."""
+
+    def __init__(self, index, cols, rows, ranks, seed=0, pad=0, plan=True):
+        gen = torch.Generator().manual_seed(seed)
+        self.index = torch.as_tensor(index, dtype=torch.int32)
+        self.t, self.cols, self.rows, self.ranks = len(self.index), cols, rows, ranks
+        n = lambda *s: torch.randn(*s, generator=gen).bfloat16()     # noqa: E731
+        self.host = dict(x=n(self.t, cols), y=n(self.t, rows), gy=n(self.t, rows), gx=n(self.t, cols))
+        self.ad = [(n(rows, r), (n(r, cols) * cols ** -0.5).bfloat16(), 2.0 / (i + 1) ** 0.5)
+                   for i, r in enumerate(ranks)]
+        self.pad = pad
+        self.dev = {k: self._wide(v) for k, v in self.host.items()}
+        self.dad = [(b.to(DEV), a.to(DEV), s) for b, a, s in self.ad]
+        self.u = torch.full((self.t + 1, qf.lora_u_cols(self.ad)), -7.0, dtype=torch.bfloat16, device=DEV)
+        self.plan = qf.qf_lora_plan(self.index.to(DEV), len(ranks)) if plan else None
+        self.ga = [torch.full_like(a, 9.0) for _, a, _ in self.dad]
+        self.gb = [torch.full_like(b, 9.0) for b, _, _ in self.dad]
+
+    def _wide(self, v):
+        """On the device, as columns of a wider buffer (pad > 0) with a marked row behind."""
+        buf = torch.full((v.shape[0] + 1, v.shape[1] + 2 * self.pad), 77.0, dtype=torch.bfloat16, device=DEV)
+        out = buf[:v.shape[0], self.pad:self.pad + v.shape[1]]
+        out.copy_(v)
+        return out
+
+    def forward(self):
+        qf.qf_lora_apply(self.dev["x"], self.dad, self.dev["y"], self.u[:self.t], plan=self.plan)
+
+    def backward(self, **kw):
+        kw = {**dict(gx=self.dev["gx"], ga=self.ga, gb=self.gb), **kw}
+        qf.qf_lora_apply_backward(self.dev["x"], self.dev["gy"], self.dad, self.u[:self.t], plan=self.plan, **kw)
+
+    def rows_of(self, i):
+        return (self.index == i).nonzero().view(-1)
+
+    def close(self, name, got, want, tol):
+        got, want, tol = got.double().cpu(), want.double(), tol.double()
+        bad = ((got - want).abs() > tol) | got.isnan()
+        assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} off, worst " \
+                              f"{float(((got - want).abs() / tol).nan_to_num(9e9).max()):.3g} of the bound"
+
+    def product(self, z, f):
+        """z f^T with its bound: FP32 sums, then BF16."""
+        p, mag = z @ f.t(), z.abs() @ f.abs().t()
+        return p, H * p.abs() + (z.shape[1] / 16 + 64) * 2.0 ** -23 * mag + 1e-30
+
+    def check_forward(self):
+        torch.cuda.synchronize()
+        y, tol = self.host["y"].double(), torch.zeros(self.t, self.rows, dtype=torch.double)
+        wide = self.u.shape[1]
+        live = torch.zeros(self.t, dtype=torch.bool)
+        for i, (b, a, s) in enumerate(self.ad):
+            r = self.rows_of(i)
+            live[r] = True
+            u, du = self.product(self.host["x"][r].double(), a.double())
+            self.close(f"u[{i}]", self.u[:self.t].cpu()[r][:, :u.shape[1]], u, du)
+            pad = self.u[:self.t].cpu()[r][:, u.shape[1]:min(wide, (u.shape[1] + 15) // 16 * 16)]
+            assert not pad.any()
+            b = b.double()
+            d, mag = u @ b.t(), (u.abs() + du) @ b.abs().t()
+            y[r] += s * d
+            tol[r] = s * (du @ b.abs().t() + (len(b.t()) / 16 + 64) * 2.0 ** -23 * mag)
+        tol = tol + H * (y.abs() + tol) + 2.0 ** -23 * y.abs()
+        tol[~live] = 0
+        self.close("y", self.dev["y"], y, tol)
+        assert bool((self.u[:self.t].cpu()[~live] == -7).all()) and bool((self.u[self.t] == -7).all())
+        self.untouched()
+
+    def check_backward(self, gx=True, factors=True):
+        torch.cuda.synchronize()
+        want, tol = self.host["gx"].double(), torch.zeros(self.t, self.cols, dtype=torch.double)
+        for i, (b, a, s) in enumerate(self.ad):
+            r = self.rows_of(i)
+            x, gy, a, b = self.host["x"][r].double(), self.host["gy"][r].double(), a.double(), b.double()
+            u, du = self.product(x, a)
+            v, dv = self.product(gy, b.t())
+            n = (len(r) / 16 + 64) * 2.0 ** -23
+            for name, got, z, w, dw, left in (("ga", self.ga[i], x, v, dv, True), ("gb", self.gb[i], gy, u, du, False)):
+                g = s * (w.t() @ z if left else z.t() @ w)
+                e = s * (dw.t() @ z.abs() if left else z.abs().t() @ dw)
+                m = s * ((w.abs() + dw).t() @ z.abs() if left else z.abs().t() @ (w.abs() + dw))
+                if factors:
+                    self.close(f"{name}[{i}]", got, g, e + n * m + H * (g.abs() + e + n * m) + 1e-30)
+                else:
+                    assert bool((got == 9).all())
+            d = s * (v @ a)
+            want[r] += d
+            e = s * (dv @ a.abs() + (a.shape[0] / 16 + 64) * 2.0 ** -23 * ((v.abs() + dv) @ a.abs()))
+            tol[r] = e
+        tol = torch.where(tol > 0, tol + H * (want.abs() + tol) + 2.0 ** -23 * want.abs(), tol)
+        self.close("gx", self.dev["gx"], want if gx else self.host["gx"], tol if gx else 0 * tol)
+        self.untouched()
+
+    def untouched(self):
+        for v in self.dev.values():
+            buf = v._base
+            assert bool((buf[-1] == 77).all()) and bool((buf[:, :self.pad] == 77).all())
+            assert bool((buf[:, buf.shape[1] - self.pad:] == 77).all())
+
+
+def spread(t, n, seed=0, none=0.2):
+    """A shuffled index with runs, strangers and tokens without an adapter."""
+    g = torch.Generator().manual_seed(seed)
+    idx = torch.randint(0, n, (t,), generator=g, dtype=torch.int32)
+    idx[torch.rand(t, generator=g) < none] = -1
+    if t > 20:
+        idx[3:t // 3] = idx[3]
+        idx[t - 1], idx[t // 2] = n, 1 << 30                       # out of range: none
+    return idx
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", [1, 2, 15, 16, 17, 63, 64, 65, 129, 700])
+@pytest.mark.parametrize("cols,rows", [(8, 8), (40, 24), (256, 264), (1000, 520)])
+def test_against_64_bits(t, cols, rows):
+    c = Batch(spread(t, 3, seed=t), cols, rows, [16, 5, 32], seed=t + cols)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rank", [1, 2, 3, 4, 7, 8, 12, 15, 16, 17, 20, 32, 33, 48, 63, 64, 65, 72, 100, 127, 128])
+def test_every_kind_of_rank(rank):
+    c = Batch(spread(150, 2, seed=rank), 328, 136, [rank, 16], seed=rank)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", [1, 100, 3000])
+def test_one_adapter_without_a_plan(t):
+    c = Batch(torch.zeros(t), 520, 1032, [24], seed=t, plan=False)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+
+
+@pytest.mark.gpu
+def test_long_and_wide():
+    c = Batch(spread(2500, 4, seed=1, none=0.02), 4096, 2056, [8, 64, 16, 40], seed=2)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+
+
+@pytest.mark.gpu
+def test_many_adapters_and_columns_of_wider_buffers():
+    idx = torch.arange(400, dtype=torch.int32) * 7 % 512
+    c = Batch(idx, 64, 72, [1 + i % 20 for i in range(512)], seed=3, pad=8)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("index", [[-1] * 70, [0] * 70, [1] * 70, list(range(-1, 69))])
+def test_adapters_without_tokens_have_zero_gradients(index):
+    c = Batch(index, 96, 80, [16, 4], seed=4)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+    for i in range(2):
+        if not (c.index == i).any():
+            assert not c.ga[i].any() and not c.gb[i].any()
+
+
+@pytest.mark.gpu
+def test_parts_of_the_backward_pass():
+    c = Batch(spread(130, 2, seed=5), 128, 96, [16, 8], seed=5)
+    c.forward()
+    c.backward(ga=None, gb=None)
+    c.check_backward(factors=False)
+    c.dev["gx"].copy_(c.host["gx"])
+    c.backward(gx=None)
+    c.check_backward(gx=False)
+
+
+@pytest.mark.gpu
+def test_no_tokens():
+    c = Batch([], 64, 48, [16, 8], seed=6)
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    assert not any(w.any() for w in c.ga + c.gb)
+
+
+@pytest.mark.gpu
+def test_a_bad_token_stays_alone():
+    """NaN and infinities in one token's x and gy reach that token's rows (and its adapter's
+    gradients), no other row."""
+    c = Batch(spread(100, 2, seed=7, none=0), 64, 64, [16, 8], seed=7)
+    clean = Batch(spread(100, 2, seed=7, none=0), 64, 64, [16, 8], seed=7)
+    for k in ("x", "gy"):
+        c.dev[k][41, 3], c.dev[k][41, 9] = float("nan"), float("inf")
+    for b in (c, clean):
+        b.forward()
+        b.backward()
+    torch.cuda.synchronize()
+    rest = torch.arange(100) != 41
+    for k in ("y", "gx"):
+        assert torch.equal(c.dev[k][rest.to(DEV)], clean.dev[k][rest.to(DEV)]) and c.dev[k][41].isnan().any()
+    other = 1 - int(c.index[41])
+    assert torch.equal(c.ga[other], clean.ga[other]) and torch.equal(c.gb[other], clean.gb[other])
+
+
+@pytest.mark.gpu
+def test_the_plan_of_another_batch_changes_nothing():
+    c = Batch(spread(100, 2, seed=8), 64, 64, [16, 8], seed=8)
+    c.plan = torch.zeros_like(c.plan)
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    assert torch.equal(c.dev["y"].cpu(), c.host["y"]) and torch.equal(c.dev["gx"].cpu(), c.host["gx"])
+    assert bool((c.u == -7).all()) and all(bool((w == 9).all()) for w in c.ga + c.gb)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,n", [(1, 1), (5, 3), (700, 7), (5000, 512), (20000, 3)])
+def test_plan_is_the_stable_sort(t, n):
+    idx = spread(t, n, seed=n, none=0.1)
+    plan = qf.qf_lora_plan(idx.to(DEV), n).cpu()
+    live = [(idx == i).nonzero().view(-1) for i in range(n)]
+    counts = torch.tensor([len(x) for x in live])
+    assert plan[1] == counts.sum() and plan[0] == ((counts + 63) // 64).sum()
+    assert torch.equal(plan[4:5 + n].long(), torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]))
+    assert torch.equal(plan[5 + n:5 + n + int(counts.sum())].long(), torch.cat(live))
+
+
+@pytest.mark.gpu
+def test_same_bits_again_and_in_a_graph_with_new_inputs():
+    """Plan, forward and backward captured once; replayed with another batch's index and
+    inputs they give what direct calls give, bit for bit."""
+    first, second = (Batch(spread(300, 3, seed=s), 512, 264, [16, 8, 20], seed=s) for s in (9, 10))
+    index = first.index.to(DEV)
+    ws = qf.alloc_lora_workspace(300, first.dad)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        qf.qf_lora_plan(index, 3, first.plan)
+        first.forward()
+        first.backward(workspace=ws)
+    for c in (Batch(spread(300, 3, seed=9), 512, 264, [16, 8, 20], seed=9), second):
+        index.copy_(c.index)
+        for k, v in first.dev.items():
+            v.copy_(c.host[k])
+        for (b, a, _), (b2, a2, _) in zip(first.dad, c.dad):
+            b.copy_(b2), a.copy_(a2)
+        first.u.fill_(-7)                    # columns behind an adapter's rank are not written
+        graph.replay()
+        c.forward()
+        c.backward()
+        torch.cuda.synchronize()
+        live = (c.index >= 0) & (c.index < 3)
+        assert torch.equal(first.u[:300][live.to(DEV)], c.u[:300][live.to(DEV)])
+        assert all(torch.equal(first.dev[k], c.dev[k]) for k in ("y", "gx"))
+        assert all(torch.equal(p, q) for p, q in zip(first.ga + first.gb, c.ga + c.gb))
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    batches = [Batch(spread(500, 2, seed=s), 256, 512, [16, 32], seed=s) for s in (11, 12)]
+    torch.cuda.synchronize()
+    for c, s in zip(batches, (torch.cuda.Stream(), torch.cuda.Stream())):
+        with torch.cuda.stream(s):
+            c.forward()
+            c.backward()
+    torch.cuda.synchronize()
+    for c in batches:
+        c.check_forward()
+        c.check_backward()
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences():
+    """y is linear in each factor, so doubling one changes <gy, y> by <gradient, factor>,
+    whatever the step.  gy is y's change itself: the sums do not cancel, and each side is
+    off by at most its BF16 roundings (y: u, y; gradients: v or u, the gradient): 4 half
+    steps, and the FP32 sums beside them, relative to the sum of magnitudes."""
+    c = Batch(torch.zeros(200), 256, 128, [16], seed=13, plan=False)
+    (b, a, s), x = c.dad[0], c.dev["x"]
+
+    def y_of(b, a):
+        y = torch.zeros(200, 128, dtype=torch.bfloat16, device=DEV)
+        qf.qf_lora_apply(x, [(b, a, s)], y)
+        return y
+    y = y_of(b, a)
+    c.u[:200] = qf.qf_lora_apply(x, c.dad, torch.zeros_like(y))
+    c.dev["gy"].copy_(y)
+    c.dev["gx"].zero_()
+    c.backward()
+    gy = y.double()
+    for name, grad, factor, moved in (("a", c.ga[0], a, y_of(b, 2 * a)), ("b", c.gb[0], b, y_of(2 * b, a)),
+                                      ("x", c.dev["gx"], x, None)):
+        if moved is None:                                           # x twice: through the input
+            moved = torch.zeros_like(y)
+            qf.qf_lora_apply(2 * x, c.dad, moved)
+        got = float((grad.double() * factor.double()).sum())
+        want = float((gy * (moved.double() - y.double())).sum())
+        mag = float((gy.abs() * y.double().abs()).sum())
+        assert abs(got - want) <= 8 * H * mag, (name, got, want)
+        assert want > 0.9 * mag
+
+
+@pytest.mark.gpu
+def test_three_dimensional_inputs_fold():
+    c = Batch(torch.zeros(12), 64, 48, [16], seed=14, plan=False)
+    x, y = c.dev["x"].contiguous().view(3, 4, 64), c.dev["y"].contiguous().view(3, 4, 48)
+    qf.qf_lora_apply(x, c.dad, y, c.u[:12])
+    c.dev["y"].copy_(y.view(12, 48))
+    c.check_forward()
+    with pytest.raises(ValueError):
+        qf.qf_lora_apply(x.transpose(0, 1), c.dad, y, c.u[:12])
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Rows whose element offset passes 2^32: the last tokens of a strided batch."""
+    t, ld = 70, 1 << 26
+    buf = torch.zeros(t * ld, dtype=torch.bfloat16, device=DEV)      # 9.4 GB
+    c = Batch(spread(t, 2, seed=15), 64, 48, [16, 8], seed=15)
+    x = buf.view(t, ld)[:, :64]
+    y = buf.view(t, ld)[:, 128:176]
+    x.copy_(c.dev["x"]), y.copy_(c.dev["y"])
+    qf.qf_lora_apply(x, c.dad, y, c.u[:t], plan=c.plan)
+    c.dev["y"].copy_(y)
+    c.check_forward()
