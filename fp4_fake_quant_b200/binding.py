@@ -595,8 +595,9 @@ def _rows(what: str, t: torch.Tensor, tokens=None, width=None):
 
 
 def lora_u_cols(adapters) -> int:
-    """Columns of the u buffer: the largest rank, rounded up to a multiple of 16."""
-    return max((int(a.shape[0]) + 15) // 16 * 16 for _, a, _ in adapters)
+    """Columns of the u buffer: twice the largest rank, rounded up to a multiple of 16 (u is
+    kept as the sum of two BF16 values)."""
+    return 2 * max((int(a.shape[0]) + 15) // 16 * 16 for _, a, _ in adapters)
 
 
 def alloc_lora_u(tokens: int, adapters) -> torch.Tensor:

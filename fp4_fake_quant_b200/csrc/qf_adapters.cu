@@ -20,7 +20,7 @@ using qf::kLoraMaxRank;
 using qf::kLoraThreads;
 using qf::kLoraTile;
 
-constexpr int kSmallA = 16, kLargeA = kLoraMaxAdapters;    // descriptor table sizes
+constexpr int kSmallA = 8, kMidA = 64, kLargeA = kLoraMaxAdapters;   // descriptor table sizes
 constexpr int64_t kMaxTokens = int64_t(1) << 26, kMaxWidth = int64_t(1) << 24;
 
 static_assert(QF_LORA_APPLY_MAX_RANK == kLoraMaxRank && QF_LORA_MAX_ADAPTERS == kLoraMaxAdapters, "");
@@ -112,65 +112,65 @@ qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, 
     return e == cudaSuccess ? QF_OK : cuda_fail(e, "cudaLaunchKernelEx");
 }
 
-#ifndef QF_LORA_CTAS
-#define QF_LORA_CTAS 592        // CTAs the split of a reduction aims at (4 per SM)
+#ifndef QF_DOWN_CTAS
+#define QF_DOWN_CTAS 296        // CTAs the split of a reduction aims at
+#endif
+#ifndef QF_GRAD_CTAS
+#define QF_GRAD_CTAS 1184
 #endif
 // Cluster size: how many CTAs share one reduction, so that `units` of them fill the GPU;
 // at most 8 (portable) and at most one per `steps` of work.
-int parts_for(int64_t units, int64_t steps) {
+int parts_for(int64_t units, int64_t steps, int64_t want) {
     int p = 1;
-    while (p < 8 && units * p < QF_LORA_CTAS && 2 * p <= steps) p *= 2;
+    while (p < 8 && units * p < want && 2 * p <= steps) p *= 2;
     return p;
-}
-
-template <int NT> constexpr size_t down_smem() {
-    return size_t(NT > 4 ? 4 : 8) * kLoraTile * (NT * 8 + 4) * sizeof(float);
 }
 
 template <int MAXA, int NT>
 qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
-               int64_t depth, bool backward, void* u, int ldu, bool dependent, cudaStream_t s) {
-    const int parts = parts_for(tiles, (depth + 255) / 256);
+               int64_t depth, bool backward, void* u, int wide, bool dependent, cudaStream_t s) {
+    const int parts = parts_for(tiles, (depth + 255) / 256, QF_DOWN_CTAS);
     if (tiles * parts > INT32_MAX) return fail(QF_ERR_SHAPE, "too many tokens for one launch");
-    return launch(qf::k_lora_down<MAXA, NT>, dim3((unsigned)(tiles * parts)), kLoraThreads, down_smem<NT>(), s,
+    return launch(qf::k_lora_down<MAXA, NT>, dim3((unsigned)(tiles * parts)), kLoraThreads, qf::DownShape<NT>::kSmem, s,
                   dependent, dim3(parts), A, P, static_cast<const uint16_t*>(z), ldz, (int)depth,
-                  (int)backward, parts, static_cast<uint16_t*>(u), ldu);
+                  (int)backward, parts, static_cast<uint16_t*>(u), wide);
 }
 template <int MAXA>
 qf_status down_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
-                   int64_t depth, bool backward, void* u, int ldu, bool dependent, cudaStream_t s) {
-    if (ldu <= 16) return down<MAXA, 2>(A, P, tiles, z, ldz, depth, backward, u, ldu, dependent, s);
-    if (ldu <= 32) return down<MAXA, 4>(A, P, tiles, z, ldz, depth, backward, u, ldu, dependent, s);
-    return down<MAXA, 8>(A, P, tiles, z, ldz, depth, backward, u, ldu, dependent, s);
+                   int64_t depth, bool backward, void* u, int wide, bool dependent, cudaStream_t s) {
+    if (wide <= 16) return down<MAXA, 2>(A, P, tiles, z, ldz, depth, backward, u, wide, dependent, s);
+    if (wide <= 32) return down<MAXA, 4>(A, P, tiles, z, ldz, depth, backward, u, wide, dependent, s);
+    return down<MAXA, 8>(A, P, tiles, z, ldz, depth, backward, u, wide, dependent, s);
 }
 
 template <int MAXA, int KS>
-qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int ldu,
+qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide,
              int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
     const int64_t blocks = tiles * ((width + 255) / 256);
     if (blocks > INT32_MAX) return fail(QF_ERR_SHAPE, "tokens x width too large for one launch");
-    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), kLoraThreads, 0, s, true, dim3(1), A, P,
-                  static_cast<const uint16_t*>(u), ldu, (int)width, (int)backward,
+    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), kLoraThreads,
+                  qf::UpShape<KS>::kSmem, s, true, dim3(1), A, P,
+                  static_cast<const uint16_t*>(u), wide, (int)width, (int)backward,
                   static_cast<uint16_t*>(y), ldy);
 }
 template <int MAXA>
-qf_status up_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int ldu,
+qf_status up_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide,
                  int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
-    if (ldu <= 16) return up<MAXA, 1>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
-    if (ldu <= 32) return up<MAXA, 2>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
-    if (ldu <= 64) return up<MAXA, 4>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
-    return up<MAXA, 8>(A, P, tiles, u, ldu, width, backward, y, ldy, s);
+    if (wide <= 16) return up<MAXA, 1>(A, P, tiles, u, wide, width, backward, y, ldy, s);
+    if (wide <= 32) return up<MAXA, 2>(A, P, tiles, u, wide, width, backward, y, ldy, s);
+    if (wide <= 64) return up<MAXA, 4>(A, P, tiles, u, wide, width, backward, y, ldy, s);
+    return up<MAXA, 8>(A, P, tiles, u, wide, width, backward, y, ldy, s);
 }
 
 template <int MAXA, int MT>
 qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf_lora_batch& c, const void* v,
-                const void* gy, int64_t ldgy, int ldu, cudaStream_t s) {
+                const void* gy, int64_t ldgy, int wide, cudaStream_t s) {
     const int64_t tiles = (c.cols + qf::kGradCols - 1) / qf::kGradCols + (c.rows + qf::kGradCols - 1) / qf::kGradCols;
-    const int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens);
+    const int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens, QF_GRAD_CTAS);
     return launch(qf::k_lora_grad<MAXA, MT>, dim3((unsigned)tiles, n, parts), qf::kGradThreads,
-                  qf::grad_smem<MT>(), s, true, dim3(1, 1, parts), G, P, static_cast<const uint16_t*>(c.x),
+                  qf::GradShape<MT>::kSmem, s, true, dim3(1, 1, parts), G, P, static_cast<const uint16_t*>(c.x),
                   c.ldx, (int)c.cols, static_cast<const uint16_t*>(v), static_cast<const uint16_t*>(gy), ldgy,
-                  (int)c.rows, static_cast<const uint16_t*>(c.u), ldu);
+                  (int)c.rows, static_cast<const uint16_t*>(c.u), wide);
 }
 
 template <int MAXA>
@@ -188,35 +188,33 @@ int64_t tiles_of(const qf_lora_batch& c, int n) {
 }
 
 template <int MAXA>
-qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int ldu, cudaStream_t s) {
+qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int wide, cudaStream_t s) {
     AdapterTable<MAXA> A;
     fill(A, l, n);
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
-    qf_status st = down_any<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, ldu, false, s);
+    qf_status st = down_any<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, wide, false, s);
     if (st != QF_OK || c.rows == 0) return st;
-    return up_any<MAXA>(A, P, tiles, c.u, ldu, c.rows, false, c.y, c.ldy, s);
+    return up_any<MAXA>(A, P, tiles, c.u, wide, c.rows, false, c.y, c.ldy, s);
 }
 
 int64_t aligned(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 template <int MAXA>
 qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora_batch& c, const void* gy,
-                   int64_t ldgy, void* gx, int64_t ldgx, void* ws, int ldu, cudaStream_t s) {
+                   int64_t ldgy, void* gx, int64_t ldgx, void* ws, int wide, cudaStream_t s) {
     qf::TurnTable<MAXA> T;
     AdapterTable<MAXA> A;
     fill(A, l, n);
     char* at = static_cast<char*>(ws);
     uint16_t* const v = reinterpret_cast<uint16_t*>(at);
-    at += aligned(2 * c.tokens * ldu);
-    int wide = 0;
+    at += aligned(4 * c.tokens * wide);
     for (int i = 0; i < n; ++i) {
         T.t[i] = A.t[i];
         T.at[i] = reinterpret_cast<uint16_t*>(at);
         at += aligned(2 * c.cols * round16(l[i].rank));
         T.bt[i] = reinterpret_cast<uint16_t*>(at);
         at += aligned(2 * c.rows * l[i].rank);
-        wide = std::max(wide, round16(l[i].rank));
     }
     const int64_t work = (c.cols + c.rows) * (wide / 8);
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((work + 255) / 256, 1024));
@@ -230,10 +228,10 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
     if (c.tokens > 0) {
-        st = down_any<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, ldu, true, s);
+        st = down_any<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, wide, true, s);
         if (st != QF_OK) return st;
         if (gx && c.cols > 0) {
-            st = up_any<MAXA>(A, P, tiles, v, ldu, c.cols, true, gx, ldgx, s);
+            st = up_any<MAXA>(A, P, tiles, v, wide, c.cols, true, gx, ldgx, s);
             if (st != QF_OK) return st;
         }
     }
@@ -244,10 +242,10 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
         G.scale[i] = l[i].scale;
         G.rank[i] = l[i].rank;
     }
-    if (ldu <= 16) return grads<MAXA, 1>(G, P, n, c, v, gy, ldgy, ldu, s);
-    if (ldu <= 32) return grads<MAXA, 2>(G, P, n, c, v, gy, ldgy, ldu, s);
-    if (ldu <= 64) return grads<MAXA, 4>(G, P, n, c, v, gy, ldgy, ldu, s);
-    return grads<MAXA, 8>(G, P, n, c, v, gy, ldgy, ldu, s);
+    if (wide <= 16) return grads<MAXA, 1>(G, P, n, c, v, gy, ldgy, wide, s);
+    if (wide <= 32) return grads<MAXA, 2>(G, P, n, c, v, gy, ldgy, wide, s);
+    if (wide <= 64) return grads<MAXA, 4>(G, P, n, c, v, gy, ldgy, wide, s);
+    return grads<MAXA, 8>(G, P, n, c, v, gy, ldgy, wide, s);
 }
 
 }  // namespace
@@ -287,15 +285,17 @@ qf_status qf_lora_apply(const qf_lora* l, int n, const qf_lora_batch* batch, voi
     int max_rank = 0;
     qf_status st = check_batch(l, n, c, &max_rank);
     if (st != QF_OK || c.tokens == 0) return st;
-    const Mat x{c.x, c.ldx, c.cols}, y{c.y, c.ldy, c.rows}, u{c.u, round16(max_rank), round16(max_rank)};
+    const Mat x{c.x, c.ldx, c.cols}, y{c.y, c.ldy, c.rows}, u{c.u, 2 * round16(max_rank), 2 * round16(max_rank)};
     if (c.cols > 0 && (st = check_mat(x, c.tokens, "x")) != QF_OK) return st;
     if (c.rows > 0 && (st = check_mat(y, c.tokens, "y")) != QF_OK) return st;
     if ((st = check_u(c)) != QF_OK) return st;
     if (share(x, y, c.tokens) || share(x, u, c.tokens) || share(y, u, c.tokens))
         return fail(QF_ERR_INVALID_ARG, "x, y and u must not overlap");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return n <= kSmallA ? apply<kSmallA>(l, n, c, round16(max_rank), s)
-                        : apply<kLargeA>(l, n, c, round16(max_rank), s);
+    const int wide = round16(max_rank);
+    return n <= kSmallA ? apply<kSmallA>(l, n, c, wide, s)
+           : n <= kMidA ? apply<kMidA>(l, n, c, wide, s)
+                        : apply<kLargeA>(l, n, c, wide, s);
 }
 
 size_t qf_lora_backward_workspace_bytes(const qf_lora* l, int n, int64_t tokens, int64_t rows, int64_t cols) {
@@ -309,7 +309,7 @@ size_t qf_lora_backward_workspace_bytes(const qf_lora* l, int n, int64_t tokens,
         max_rank = std::max(max_rank, (int)l[i].rank);
         bytes += aligned(2 * cols * round16(l[i].rank)) + aligned(2 * rows * l[i].rank);
     }
-    return (size_t)(bytes + aligned(2 * tokens * round16(max_rank)));
+    return (size_t)(bytes + aligned(4 * tokens * round16(max_rank)));
 }
 
 qf_status qf_lora_apply_backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora_batch* batch,
@@ -322,8 +322,8 @@ qf_status qf_lora_apply_backward(const qf_lora* l, const qf_lora_grad* g, int n,
     qf_status st = check_batch(l, n, c, &max_rank);
     if (st != QF_OK) return st;
     if (gx == nullptr && g == nullptr) return fail(QF_ERR_INVALID_ARG, "no output: gx and g are NULL");
-    const int ldu = round16(max_rank);
-    const Mat x{c.x, c.ldx, c.cols}, u{c.u, ldu, ldu}, my{gy, ldgy, c.rows}, mx{gx, ldgx, c.cols};
+    const int wide = round16(max_rank);
+    const Mat x{c.x, c.ldx, c.cols}, u{c.u, 2 * wide, 2 * wide}, my{gy, ldgy, c.rows}, mx{gx, ldgx, c.cols};
     if (c.tokens > 0) {
         if (c.rows > 0 && (st = check_mat(my, c.tokens, "gy")) != QF_OK) return st;
         if (gx && c.cols > 0 && (st = check_mat(mx, c.tokens, "gx")) != QF_OK) return st;
@@ -342,8 +342,9 @@ qf_status qf_lora_apply_backward(const qf_lora* l, const qf_lora_grad* g, int n,
                     d_workspace ? workspace_bytes : (size_t)0, need);
     if (!aligned16(d_workspace)) return fail(QF_ERR_ALIGN, "workspace not 16-byte aligned");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return n <= kSmallA ? backward<kSmallA>(l, g, n, c, gy, ldgy, gx, ldgx, d_workspace, ldu, s)
-                        : backward<kLargeA>(l, g, n, c, gy, ldgy, gx, ldgx, d_workspace, ldu, s);
+    return n <= kSmallA ? backward<kSmallA>(l, g, n, c, gy, ldgy, gx, ldgx, d_workspace, wide, s)
+           : n <= kMidA ? backward<kMidA>(l, g, n, c, gy, ldgy, gx, ldgx, d_workspace, wide, s)
+                        : backward<kLargeA>(l, g, n, c, gy, ldgy, gx, ldgx, d_workspace, wide, s);
 }
 
 }  // extern "C"

@@ -507,7 +507,7 @@ size_t qf_grad_norm_workspace_bytes(void);
  *
  * With adapter i = l[index[t]] of token t (b [rows, rank], a [rank, cols], scale; BF16,
  * a 16-byte aligned; rank 1 .. QF_LORA_APPLY_MAX_RANK, the adapters' ranks may differ):
- *   u[t] = BF16( sum over c of x[t,c] a[k,c] ),  k < rank
+ *   u[t] = sum over c of x[t,c] a[k,c],  k < rank, kept as the sum of two BF16 values
  *   y[t] = BF16( y[t] + scale * sum over k of u[t,k] b[r,k] ),  r < rows
  * Sums in FP32 on the tensor cores, in an order that is fixed for a device, so equal calls
  * give equal bits.  A token without an adapter is left as it was (y, u, gx).
@@ -533,9 +533,10 @@ size_t qf_lora_plan_bytes(int64_t tokens, int n_adapters);     /* 0 for sizes ou
  *   x       BF16 [tokens, cols], row stride ldx elements: the projection's input
  *   y       BF16 [tokens, rows], row stride ldy: the shared projection's output, added to
  *           in place (qf_lora_apply only)
- *   u       BF16 [tokens, R], contiguous, R = the largest rank rounded up to a multiple of
- *           16: written by qf_lora_apply (each token's columns up to its adapter's rank, and
- *           zeros up to the next multiple of 16), read by qf_lora_apply_backward
+ *   u       BF16 [tokens, 2 R], contiguous, R = the largest rank rounded up to a multiple of
+ *           16: written by qf_lora_apply, read by qf_lora_apply_backward.  u's columns
+ *           rounded to BF16, then at R what is left, rounded too: 17 significant bits.  Of a
+ *           token, its adapter's columns are written (zeros up to a multiple of 16).
  *   rows, cols   multiples of 8, at most 2^24
  *   d_plan  from qf_lora_plan for the same tokens and number of adapters (for other sizes
  *           the call leaves its outputs as they were), or NULL: one adapter, every token
@@ -570,7 +571,7 @@ typedef struct qf_lora_grad {
 
 /*
  * qf_lora_apply_backward -- with gy the gradient of y:
- *   v[t]   = BF16( sum over r of gy[t,r] b[r,k] )
+ *   v[t]   = sum over r of gy[t,r] b[r,k], kept like u
  *   gx[t]  = BF16( gx[t] + scale * sum over k of v[t,k] a[k,c] )
  *   ga     = BF16( scale * sum over the adapter's tokens of v[t,k] x[t,c] )
  *   gb     = BF16( scale * sum over the adapter's tokens of gy[t,r] u[t,k] )

@@ -2,8 +2,8 @@
 closeness to the formulas in 64 bits at the sizes, ranks, orders and strides where they can
 go wrong, gradients against differences, rows without an adapter, graphs and streams.
 
-Tolerances count roundings: u and v are rounded to BF16 (half a step, 2^-8 relative), outputs
-too; FP32 sums of n products on the tensor cores are within (n / 16 + 64) 2^-23 of the sum of
+Tolerances count roundings: u and v are two BF16 values each, half a step of the second being
+2^-8 of 2^-8 of the value; outputs are rounded to BF16 (half a step, 2^-8 relative); FP32 sums of n products on the tensor cores are within (n / 16 + 64) 2^-23 of the sum of
 their magnitudes (one addition per MMA, sixteen products inside one, and up to 64 partial
 sums joined)."""
 import ctypes
@@ -113,7 +113,7 @@ def test_nothing_to_do():
 def test_binding_refusals():
     x, y = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, 8, dtype=torch.bfloat16)
     ad = [(torch.zeros(8, 2, dtype=torch.bfloat16), torch.zeros(2, 16, dtype=torch.bfloat16), 1.0)]
-    u = torch.zeros(4, 16, dtype=torch.bfloat16)
+    u = torch.zeros(4, 32, dtype=torch.bfloat16)
     with pytest.raises(ValueError):                               # not on a GPU
         qf.qf_lora_apply(x, ad, y, u)
     with pytest.raises(ValueError):
@@ -122,7 +122,7 @@ def test_binding_refusals():
         qf.qf_lora_apply(x, [(ad[0][0], ad[0][1][:, :8], 1.0), ad[0]], y, u)
     with pytest.raises(TypeError):
         qf.qf_lora_plan(torch.zeros(4, dtype=torch.int64), 1, torch.zeros(64, dtype=torch.int32))
-    assert qf.lora_u_cols(ad) == 16
+    assert qf.lora_u_cols(ad) == 32
 
 
 # ------------------------------------------------------------------ the batch and its reference
@@ -170,9 +170,9 @@ class Batch:
                               f"{float(((got - want).abs() / tol).nan_to_num(9e9).max()):.3g} of the bound"
 
     def product(self, z, f):
-        """z f^T with its bound: FP32 sums, then BF16."""
+        """z f^T with its bound: FP32 sums, then two BF16 values."""
         p, mag = z @ f.t(), z.abs() @ f.abs().t()
-        return p, H * p.abs() + (z.shape[1] / 16 + 64) * 2.0 ** -23 * mag + 1e-30
+        return p, H * H * p.abs() + (z.shape[1] / 16 + 64) * 2.0 ** -23 * mag + 1e-30
 
     def check_forward(self):
         torch.cuda.synchronize()
@@ -183,9 +183,11 @@ class Batch:
             r = self.rows_of(i)
             live[r] = True
             u, du = self.product(self.host["x"][r].double(), a.double())
-            self.close(f"u[{i}]", self.u[:self.t].cpu()[r][:, :u.shape[1]], u, du)
-            pad = self.u[:self.t].cpu()[r][:, u.shape[1]:min(wide, (u.shape[1] + 15) // 16 * 16)]
-            assert not pad.any()
+            k, end = u.shape[1], (u.shape[1] + 15) // 16 * 16
+            parts = self.u[:self.t].cpu()[r].double()
+            hi, lo = parts[:, :wide // 2], parts[:, wide // 2:]
+            self.close(f"u[{i}]", (hi + lo)[:, :k], u, du)
+            assert not hi[:, k:end].any() and not lo[:, k:end].any()
             b = b.double()
             d, mag = u @ b.t(), (u.abs() + du) @ b.abs().t()
             y[r] += s * d
@@ -359,9 +361,13 @@ def test_plan_is_the_stable_sort(t, n):
     plan = qf.qf_lora_plan(idx.to(DEV), n).cpu()
     live = [(idx == i).nonzero().view(-1) for i in range(n)]
     counts = torch.tensor([len(x) for x in live])
-    assert plan[1] == counts.sum() and plan[0] == ((counts + 63) // 64).sum()
+    assert plan[1] == counts.sum()
     assert torch.equal(plan[4:5 + n].long(), torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]))
     assert torch.equal(plan[5 + n:5 + n + int(counts.sum())].long(), torch.cat(live))
+    tiles = plan[5 + n + t:].view(-1, 2)[:plan[0]].tolist()                # adapter or -1, begin
+    start = [0] + counts.cumsum(0).tolist()
+    assert [x for x in tiles if x[0] >= 0] == [[i, start[i] + k] for i in range(n)
+                                               for k in range(0, int(counts[i]), 64)]
 
 
 @pytest.mark.gpu
@@ -412,8 +418,8 @@ def test_two_streams_at_once():
 def test_gradients_against_differences():
     """y is linear in each factor, so doubling one changes <gy, y> by <gradient, factor>,
     whatever the step.  gy is y's change itself: the sums do not cancel, and each side is
-    off by at most its BF16 roundings (y: u, y; gradients: v or u, the gradient): 4 half
-    steps, and the FP32 sums beside them, relative to the sum of magnitudes."""
+    off by at most its BF16 roundings (y twice, the gradient once): 3 half steps, and one for
+    the FP32 sums beside them, relative to the sum of magnitudes."""
     c = Batch(torch.zeros(200), 256, 128, [16], seed=13, plan=False)
     (b, a, s), x = c.dad[0], c.dev["x"]
 
@@ -435,7 +441,7 @@ def test_gradients_against_differences():
         got = float((grad.double() * factor.double()).sum())
         want = float((gy * (moved.double() - y.double())).sum())
         mag = float((gy.abs() * y.double().abs()).sum())
-        assert abs(got - want) <= 8 * H * mag, (name, got, want)
+        assert abs(got - want) <= 4 * H * mag, (name, got, want)
         assert want > 0.9 * mag
 
 
