@@ -126,27 +126,20 @@ int parts_for(int64_t units, int64_t steps, int64_t want) {
     return p;
 }
 
-template <int MAXA, int NT>
+template <int MAXA>
 qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
                int64_t depth, bool backward, void* u, int wide, bool dependent, cudaStream_t s) {
     const int parts = parts_for(tiles, (depth + 255) / 256, QF_DOWN_CTAS);
     if (tiles * parts > INT32_MAX) return fail(QF_ERR_SHAPE, "too many tokens for one launch");
-    return launch(qf::k_lora_down<MAXA, NT>, dim3((unsigned)(tiles * parts)), kLoraThreads, qf::DownShape<NT>::kSmem, s,
+    return launch(qf::k_lora_down<MAXA>, dim3((unsigned)(tiles * parts)), qf::kTcThreads, qf::down_smem(wide), s,
                   dependent, dim3(parts), A, P, static_cast<const uint16_t*>(z), ldz, (int)depth,
                   (int)backward, parts, static_cast<uint16_t*>(u), wide);
-}
-template <int MAXA>
-qf_status down_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
-                   int64_t depth, bool backward, void* u, int wide, bool dependent, cudaStream_t s) {
-    if (wide <= 16) return down<MAXA, 2>(A, P, tiles, z, ldz, depth, backward, u, wide, dependent, s);
-    if (wide <= 32) return down<MAXA, 4>(A, P, tiles, z, ldz, depth, backward, u, wide, dependent, s);
-    return down<MAXA, 8>(A, P, tiles, z, ldz, depth, backward, u, wide, dependent, s);
 }
 
 template <int MAXA, int KS>
 qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide,
              int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
-    const int64_t blocks = tiles * ((width + 255) / 256);
+    const int64_t blocks = tiles * (kLoraTile / qf::kUpTile) * ((width + 255) / 256);
     if (blocks > INT32_MAX) return fail(QF_ERR_SHAPE, "tokens x width too large for one launch");
     return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), kLoraThreads,
                   qf::UpShape<KS>::kSmem, s, true, dim3(1), A, P,
@@ -162,13 +155,13 @@ qf_status up_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, 
     return up<MAXA, 8>(A, P, tiles, u, wide, width, backward, y, ldy, s);
 }
 
-template <int MAXA, int MT>
+template <int MAXA>
 qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf_lora_batch& c, const void* v,
                 const void* gy, int64_t ldgy, int wide, cudaStream_t s) {
     const int64_t tiles = (c.cols + qf::kGradCols - 1) / qf::kGradCols + (c.rows + qf::kGradCols - 1) / qf::kGradCols;
     const int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens, QF_GRAD_CTAS);
-    return launch(qf::k_lora_grad<MAXA, MT>, dim3((unsigned)tiles, n, parts), qf::kGradThreads,
-                  qf::GradShape<MT>::kSmem, s, true, dim3(1, 1, parts), G, P, static_cast<const uint16_t*>(c.x),
+    return launch(qf::k_lora_grad<MAXA>, dim3((unsigned)tiles, n, parts), qf::kTcThreads,
+                  qf::grad_smem(wide), s, true, dim3(1, 1, parts), G, P, static_cast<const uint16_t*>(c.x),
                   c.ldx, (int)c.cols, static_cast<const uint16_t*>(v), static_cast<const uint16_t*>(gy), ldgy,
                   (int)c.rows, static_cast<const uint16_t*>(c.u), wide);
 }
@@ -193,7 +186,7 @@ qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int wide, cudaS
     fill(A, l, n);
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
-    qf_status st = down_any<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, wide, false, s);
+    qf_status st = down<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, wide, false, s);
     if (st != QF_OK || c.rows == 0) return st;
     return up_any<MAXA>(A, P, tiles, c.u, wide, c.rows, false, c.y, c.ldy, s);
 }
@@ -228,7 +221,7 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
     if (c.tokens > 0) {
-        st = down_any<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, wide, true, s);
+        st = down<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, wide, true, s);
         if (st != QF_OK) return st;
         if (gx && c.cols > 0) {
             st = up_any<MAXA>(A, P, tiles, v, wide, c.cols, true, gx, ldgx, s);
@@ -242,10 +235,7 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
         G.scale[i] = l[i].scale;
         G.rank[i] = l[i].rank;
     }
-    if (wide <= 16) return grads<MAXA, 1>(G, P, n, c, v, gy, ldgy, wide, s);
-    if (wide <= 32) return grads<MAXA, 2>(G, P, n, c, v, gy, ldgy, wide, s);
-    if (wide <= 64) return grads<MAXA, 4>(G, P, n, c, v, gy, ldgy, wide, s);
-    return grads<MAXA, 8>(G, P, n, c, v, gy, ldgy, wide, s);
+    return grads<MAXA>(G, P, n, c, v, gy, ldgy, wide, s);
 }
 
 }  // namespace

@@ -13,7 +13,7 @@
 
 namespace qf {
 
-constexpr int kLoraTile = 64;           // tokens of one tile (all of one adapter)
+constexpr int kLoraTile = 128;          // tokens of one tile (all of one adapter)
 constexpr int kLoraMaxAdapters = 512;
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraThreads = 256;
@@ -55,7 +55,7 @@ __device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcon
 // Sorts the tokens by adapter (stable) and cuts each adapter's run into tiles.  One CTA
 // per adapter: its warps count, over consecutive ranges of tokens, those of smaller
 // adapters and their own, note which adapters occur, and place their own by the ballots'
-// ranks.  An adapter's first tile is start / 64 + the adapters that occur before it, which
+// ranks.  An adapter's first tile is start / 128 + the adapters that occur before it, which
 // leaves room for each run's short last tile without knowing the other runs' lengths;
 // slots left over are empty tiles.  Latency-bound: every CTA reads the index from L2.
 __global__ void __launch_bounds__(kPlanThreads)
@@ -242,148 +242,244 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     return v;
 }
 
+// ---------------------------------------------------------------- tcgen05
+//
+// Waits on shared-memory barriers are bounded: a thread that gives up marks the CTA, whose
+// results then become NaN.  (Nothing but this CTA's own copies and MMAs arrives there.)
+constexpr int kBarrierTries = 1 << 22;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void barrier_init(uint64_t* bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint64_t* bar) {
+    asm volatile("{ .reg .b64 t; mbarrier.arrive.shared::cta.b64 t, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ bool barrier_wait(uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < kBarrierTries; ++i) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t* out, int cols) {       // one whole warp
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(out)),
+                 "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, int cols) {          // the same warp
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+__device__ __forceinline__ int tmem_cols(int n) {                           // a power of two, at least 32
+    int c = 32;
+    while (c < n) c *= 2;
+    return c;
+}
+// Shared-memory operand in the 128-byte swizzle: rows of 128 bytes in groups of eight
+// (1024 bytes, `group` apart); `block`: distance of the next 64 elements of a row that is
+// longer (only where the row runs along M or N).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t block, uint32_t group) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(block >> 4) << 16 | (uint64_t)(group >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// BF16 operands, FP32 accumulator, M = 128; turned: both operands have K as their rows.
+__device__ __forceinline__ uint32_t mma_shape(int n, bool turned) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (turned ? 3u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void mma_tc(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(shape),
+                 "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {                 // arrives when all MMAs so far are done
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t at, float* v) {        // 16 columns of the warp's 32 rows
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void writes_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One CTA's product in TMEM: four warps copy (they gather rows, so by cp.async, 16 bytes a
+// thread, into the swizzled layout), the fifth warp's first lane issues the MMAs.  A stage
+// is full when its 128 copiers have seen their copies arrive and have fenced them for the
+// tensor core's proxy, STAGES - 1 stages after they issued them; it is empty when its MMAs
+// have committed.  FETCH(i, base) issues one thread's copies of step i; MMA(i, base) one
+// step's MMAs.  Returns false in the copiers if a wait gave up.
+constexpr int kTcThreads = 160, kCopiers = 128;
+template <int ST>
+struct TcPipe {
+    uint64_t full[ST], empty[ST], done;
+    uint32_t tmem;
+    int dead;
+    __device__ __forceinline__ void start(int cols) {       // every thread; ends with a barrier
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int i = 0; i < ST; ++i) {
+                barrier_init(&full[i], kCopiers);
+                barrier_init(&empty[i], 1);
+            }
+            barrier_init(&done, 1);
+            dead = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        if (threadIdx.x >= kCopiers) tmem_alloc(&tmem, cols);
+        before_sync();
+        __syncthreads();
+        after_sync();
+    }
+    template <typename FETCH>
+    __device__ __forceinline__ void copy(int steps, uint32_t base, uint32_t stage, FETCH fetch) {
+        bool ok = true;
+        for (int i = 0; i < steps + ST - 1 && ok; ++i) {
+            const int s = i % ST;
+            if (i < steps) {
+                if (i >= ST) ok = barrier_wait(&empty[s], (i / ST - 1) & 1);
+                if (ok) fetch(i, base + s * stage);
+            }
+            cp_async_commit();
+            if (i >= ST - 1) {
+                cp_async_wait<ST - 1>();
+                writes_to_async();
+                barrier_arrive(&full[(i - (ST - 1)) % ST]);
+            }
+        }
+        cp_async_wait<0>();
+        if (!ok || !barrier_wait(&done, 0)) dead = 1;
+    }
+    template <typename MMA>
+    __device__ __forceinline__ void multiply(int steps, uint32_t base, uint32_t stage, MMA mma) {
+        if (threadIdx.x == kCopiers) {
+            for (int i = 0; i < steps; ++i) {
+                if (!barrier_wait(&full[i % ST], (i / ST) & 1)) {
+                    dead = 1;
+                    break;
+                }
+                after_sync();
+                mma(i, base + (i % ST) * stage);
+                mma_commit(&empty[i % ST]);
+            }
+            mma_commit(&done);
+        }
+    }
+    __device__ __forceinline__ void finish(int cols) {      // after a barrier of all threads
+        if (threadIdx.x >= kCopiers) tmem_free(tmem, cols);
+    }
+};
+
 // ---------------------------------------------------------------- down: u = z F^T
 //
 // z [tokens, depth] (row stride ldz), F the factor with the reduction index contiguous
 // ([rank, depth], row stride depth), u [tokens, 2 wide] BF16: the sums as two BF16 values,
 // the high parts first, because they are the next products' operands (one BF16 value
 // would cost the gradients as much again as their own rounding).
-// A CTA takes one tile and a slice of depth; the CTAs of a cluster take the slices of one
-// tile and add their sums through distributed shared memory in rank order, so the result
-// does not depend on timing.  Within a CTA the warps are split WM over the tile's tokens
-// and WK over depth.  z and F stream through a ring of shared memory that belongs to the
-// lane: a lane copies (cp.async) exactly the 16 bytes it will read back as fragments, so
-// the copies run STAGES - 1 steps ahead without registers and without any barrier.
-// NT: 8-wide rank tiles per pass (ranks above 64 take passes of 64).
+// A CTA takes one tile (128 rows = the MMA's M, the rank is its N) and a slice of depth,
+// 64 columns a step; the CTAs of a cluster take the slices of one tile and add their sums
+// through distributed shared memory in rank order, so the result does not depend on timing.
+// Rows behind the tile's last are not loaded: what lies there only reaches their own rows.
 #ifndef QF_DOWN_STAGES
-#define QF_DOWN_STAGES 3
+#define QF_DOWN_STAGES 4
 #endif
-template <int NT> struct DownShape {
-    static constexpr int WM = NT > 4 ? 2 : 1, WK = 8 / WM, MB = 4 / WM, RW = NT * 8 + 4;
-    static constexpr int kFrags = 2 * MB + NT;           // 16-byte vectors a lane holds per step
-    static constexpr size_t kRing = size_t(8) * QF_DOWN_STAGES * kFrags * 512;
-    static constexpr size_t kRed = size_t(WK) * kLoraTile * RW * sizeof(float);
-    static constexpr size_t kSmem = kRing > kRed ? kRing : kRed;
-};
-template <int MAXA, int NT>
-__global__ void __launch_bounds__(kLoraThreads)
+__host__ __device__ constexpr uint32_t down_stage(int wide) { return kLoraTile * 128 + wide * 128; }
+constexpr size_t down_smem(int wide) {
+    const size_t pipe = size_t(QF_DOWN_STAGES) * down_stage(wide), red = size_t(kLoraTile) * (wide + 4) * 4;
+    return (pipe > red ? pipe : red) + 1024;
+}
+template <int MAXA>
+__global__ void __launch_bounds__(kTcThreads)
 k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const uint16_t* __restrict__ z,
             int64_t ldz, int depth, int backward, int parts, uint16_t* __restrict__ u, int wide_max) {
-    using S = DownShape<NT>;
-    constexpr int WM = S::WM, WK = S::WK, MB = S::MB, RW = S::RW, ST = QF_DOWN_STAGES;
-    extern __shared__ __align__(16) unsigned char smem[];
-    float* const red = reinterpret_cast<float*>(smem);   // [WK][64][RW], after the ring's use
+    extern __shared__ unsigned char raw[];
+    __shared__ TcPipe<QF_DOWN_STAGES> pipe;
     wait_previous_grid();
     let_next_grid_start();
     const Tile tile = tile_of(P, blockIdx.x / parts);     // parts = the cluster size
     if (tile.count <= 0) return;                         // the same for the whole cluster
     const Adapter ad = A.t[tile.adapter];
-    const uint16_t* const f = backward ? ad.b : ad.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-    const int wm = warp % WM, wk = warp / WM, row0 = wm * MB * 16;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * ST * S::kFrags * 512 + lane * 16;
-    const uint16_t* zr[MB][2];
+    const int wide = (ad.rank + 15) / 16 * 16, cols = tmem_cols(wide), tid = threadIdx.x;
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, stage = down_stage(wide);
+    float* const red = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
+    const int RW = wide + 4;
+    pipe.start(cols);
+    const int steps = (depth + 63) / 64, per = (steps + parts - 1) / parts;
+    const int first = min(steps, (int)(blockIdx.x % parts) * per), mine = min(steps, first + per) - first;
+    if (tid < kCopiers) {
+        const uint16_t* const f = backward ? ad.b : ad.a;
+        const int c = tid & 7, row = tid >> 3;            // 16-byte column, first of every 16th row
+        const uint32_t at = row * 128 + ((c ^ (row & 7)) << 4);
+        const uint16_t* zr[8];
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = row0 + m * 16 + h * 8 + g;     // rows behind the tile repeat its first
-            zr[m][h] = z + (int64_t)tile.token(i < tile.count ? i : 0) * ldz + 8 * q;
+        for (int k = 0; k < 8; ++k) {
+            const int i = row + 16 * k;
+            zr[k] = i < tile.count ? z + (int64_t)tile.token(i) * ldz : nullptr;
         }
-    const int steps = (depth + 31) / 32, per = (steps + parts - 1) / parts;
-    const int first = (int)(blockIdx.x % parts) * per, last = min(steps, first + per);
-    const int wide = (ad.rank + 15) / 16 * 16;           // columns of u this adapter owns
-    for (int r0 = 0; r0 < wide; r0 += NT * 8) {
-        float acc[MB][NT][4] = {};
-        const uint16_t* fr[NT];
+        pipe.copy(mine, base, stage, [&](int i, uint32_t to) {
+            const int k0 = (first + i) * 64 + c * 8;
+            const bool in = k0 < depth;
+            const int off = in ? k0 : 0;                  // (a zero-filled copy reads nothing)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int r = r0 + 8 * j + g;
-            fr[j] = f + (int64_t)(r < ad.rank ? r : 0) * depth + 8 * q;
-        }
-        auto fetch = [&](int c, uint32_t at) {
-            if (c < last) {
-                const bool in = 32 * c + 8 * q < depth;
-                const int off = in ? 32 * c : 0;         // (a zero-filled copy reads nothing)
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (row0 + m * 16 < tile.count) cp_async16(at + (2 * m + h) * 512, zr[m][h] + off, in);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    if (r0 + 8 * j < ad.rank)
-                        cp_async16(at + (2 * MB + j) * 512, fr[j] + off, in && r0 + 8 * j + g < ad.rank);
+            for (int k = 0; k < 8; ++k)
+                if (zr[k]) cp_async16(to + at + k * 2048, zr[k] + off, in);
+            for (int k = 0; k < wide / 16; ++k) {
+                const int r = row + 16 * k;
+                const bool live = in && r < ad.rank;
+                cp_async16(to + kLoraTile * 128 + at + k * 2048, f + (live ? (int64_t)r * depth + off : 0), live);
             }
-            cp_async_commit();
-        };
+        });
+    } else {
+        const uint32_t shape = mma_shape(wide, false);
+        pipe.multiply(mine, base, stage, [&](int i, uint32_t from) {
 #pragma unroll
-        for (int s = 0; s < ST - 1; ++s) fetch(first + wk + s * WK, ring + s * S::kFrags * 512);
-        uint32_t read = ring, write = ring + (ST - 1) * S::kFrags * 512;
-        for (int c = first + wk; c < last; c += WK) {
-            fetch(c + (ST - 1) * WK, write);
-            cp_async_wait<ST - 1>();
-            uint4 fv[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if (r0 + 8 * j < ad.rank) fv[j] = lds16(read + (2 * MB + j) * 512);
-#pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                if (row0 + m * 16 >= tile.count) continue;
-                const uint4 z0 = lds16(read + 2 * m * 512), z1 = lds16(read + (2 * m + 1) * 512);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if (r0 + 8 * j >= ad.rank) continue;
-                    mma_bf16(acc[m][j], z0.x, z1.x, z0.y, z1.y, fv[j].x, fv[j].y);
-                    mma_bf16(acc[m][j], z0.z, z1.z, z0.w, z1.w, fv[j].z, fv[j].w);
-                }
-            }
-            write = read;
-            read += S::kFrags * 512;
-            if (read == ring + ST * S::kFrags * 512) read = ring;
-        }
-        cp_async_wait<0>();
-        __syncthreads();                                 // the ring becomes the reduction's buffer
-        float* const mine = red + (int64_t)(wk * kLoraTile) * RW;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            if (row0 + m * 16 >= tile.count) continue;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float* const at = mine + (row0 + m * 16 + g) * RW + 8 * j + 2 * q;
-                *reinterpret_cast<float2*>(at) = make_float2(acc[m][j][0], acc[m][j][1]);
-                *reinterpret_cast<float2*>(at + 8 * RW) = make_float2(acc[m][j][2], acc[m][j][3]);
-            }
-        }
-        __syncthreads();
-        const int quads = min(NT * 8, wide - r0) / 4;
-        for (int i = threadIdx.x; i < tile.count * quads; i += kLoraThreads) {
-            float* const at = red + (i / quads) * RW + i % quads * 4;
-            float4 s = *reinterpret_cast<const float4*>(at);
-#pragma unroll
-            for (int w = 1; w < WK; ++w) {
-                const float4 t = *reinterpret_cast<const float4*>(at + w * kLoraTile * RW);
-                s.x += t.x;
-                s.y += t.y;
-                s.z += t.z;
-                s.w += t.w;
-            }
-            *reinterpret_cast<float4*>(at) = s;
-        }
-        if (parts > 1) cluster_sync(); else __syncthreads();
-        const int me = parts > 1 ? (int)cluster_rank() : 0;
-        for (int i = me * kLoraThreads + threadIdx.x; i < tile.count * quads; i += parts * kLoraThreads) {
-            const int t = i / quads, r = i % quads * 4;
-            const float* const at = red + t * RW + r;
-            const float4 s = parts > 1 ? sum_cluster(at, parts) : *reinterpret_cast<const float4*>(at);
-            uint2 hi, lo;
-            split_bf16(s, &hi, &lo);
-            uint16_t* const out = u + (int64_t)tile.token(t) * 2 * wide_max + r0 + r;
-            *reinterpret_cast<uint2*>(out) = hi;
-            *reinterpret_cast<uint2*>(out + wide_max) = lo;
-        }
-        if (parts > 1) cluster_sync(); else __syncthreads();
+            for (int k = 0; k < 4; ++k)
+                mma_tc(pipe.tmem, operand(from + 32 * k, 16, 1024), operand(from + kLoraTile * 128 + 32 * k, 16, 1024),
+                       shape, i > 0 || k > 0);
+        });
     }
+    __syncthreads();                                      // (the copiers have seen the last MMA)
+    after_sync();
+    const bool bad = pipe.dead != 0;
+    const int warp = tid >> 5;
+    if (warp < 4 && 32 * warp < tile.count) {
+        float v[16];
+        for (int n = 0; n < wide; n += 16) {
+            if (mine > 0) {
+                tmem_load16(pipe.tmem + (warp << 21) + n, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(red + tid * RW + n + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+    }
+    before_sync();
+    if (parts > 1) cluster_sync(); else __syncthreads();
+    pipe.finish(cols);
+    const int quads = wide / 4, me = parts > 1 ? (int)cluster_rank() : 0;
+    for (int i = me * kTcThreads + tid; i < tile.count * quads; i += parts * kTcThreads) {
+        const int t = i / quads, r = i % quads * 4;
+        float4 s = parts > 1 ? sum_cluster(red + t * RW + r, parts) : *reinterpret_cast<const float4*>(red + t * RW + r);
+        if (bad) s.x = s.y = s.z = s.w = __int_as_float(0x7FC00000);
+        uint2 hi, lo;
+        split_bf16(s, &hi, &lo);
+        uint16_t* const out = u + (int64_t)tile.token(t) * 2 * wide_max + r;
+        *reinterpret_cast<uint2*>(out) = hi;
+        *reinterpret_cast<uint2*>(out + wide_max) = lo;
+    }
+    if (parts > 1) cluster_sync();                        // its shared memory may still be read
 }
 
 // ---------------------------------------------------------------- up: y += s u F^T
@@ -396,9 +492,10 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
 // 64 bytes per row.  All of the tile's y is on its way (cp.async, each lane what it will
 // read itself) before the first product; u comes once per CTA.
 // KS: 16-deep rank steps.
+constexpr int kUpTile = 64;             // tokens of one CTA: half a tile
 template <int KS> struct UpShape {
     static constexpr int kRow = 2 * KS * 16 + 8;          // u's row in shared memory, padded
-    static constexpr size_t kSmem = size_t(kLoraTile) * kRow * 2 + size_t(8) * 8 * 512;
+    static constexpr size_t kSmem = size_t(kUpTile) * kRow * 2 + size_t(8) * 8 * 512;
 };
 template <int MAXA, int KS>
 __global__ void __launch_bounds__(kLoraThreads)
@@ -409,14 +506,17 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
     wait_previous_grid();
     let_next_grid_start();
     const int across = (width + 255) / 256;
-    const Tile tile = tile_of(P, blockIdx.x / across);
+    Tile tile = tile_of(P, blockIdx.x / across / 2);
+    const int part = blockIdx.x / across % 2 * kUpTile;
+    tile.begin += part;
+    tile.count = min(tile.count - part, kUpTile);
     if (tile.count <= 0) return;
     const Adapter ad = A.t[tile.adapter];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int n0 = (int)(blockIdx.x % across) * 256 + warp * 32, col = n0 + 8 * q;
     const int ks = (ad.rank + 15) / 16;
     const uint32_t us = (uint32_t)__cvta_generic_to_shared(smem);
-    const uint32_t ys = us + kLoraTile * UR * 2 + warp * 8 * 512 + lane * 16;
+    const uint32_t ys = us + kUpTile * UR * 2 + warp * 8 * 512 + lane * 16;
     for (int i = threadIdx.x; i < tile.count * ks * 4; i += kLoraThreads) {
         const int t = i / (ks * 4), c = i % (ks * 4) * 8;          // high parts, then low parts
         const int half = c >= ks * 16;
@@ -531,10 +631,10 @@ k_lora_turn(const __grid_constant__ TurnTable<MAXA> A, int rows, int cols) {
 //
 // gA = s v^T x ([rank, cols]) and gB = s gy^T u ([rows, rank]): the reduction runs over an
 // adapter's tokens.  One launch for both: blockIdx.x walks 128-column tiles of x, then of
-// gy.  A CTA stages 32 tokens at a time (rows gathered by the plan) through four cp.async
-// buffers and multiplies with the rank as the MMA's rows, so rank 16 fills it; both operands
-// have the token index outermost and come through ldmatrix.trans.  The CTAs of a cluster
-// take slices of the tokens and add up through distributed shared memory in rank order.
+// gy.  The columns are the MMA's M, the high and low parts of v or u side by side its N, 64
+// gathered tokens a step its K; both operands lie in shared memory as in HBM, tokens
+// outermost, which the tensor core reads turned.  The CTAs of a cluster take slices of the
+// tokens and add up through distributed shared memory in rank order.
 struct GradOut {
     void* ga;
     void* gb;
@@ -545,115 +645,93 @@ struct GradTable {
     float scale[MAXA];
     int rank[MAXA];
 };
-constexpr int kGradCols = 128, kGradTokens = 32, kGradStages = 4, kGradThreads = 128;
-
-__device__ __forceinline__ void ldmatrix_t(uint32_t* r, const uint16_t* p) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"((uint32_t)__cvta_generic_to_shared(p)) : "memory");
+constexpr int kGradCols = 128, kGradTokens = 64;
+#ifndef QF_GRAD_STAGES
+#define QF_GRAD_STAGES 4
+#endif
+constexpr uint32_t kGradBlock = kGradTokens * 128;         // 64 columns of a stage
+__host__ __device__ constexpr uint32_t grad_stage(int wide) { return kGradBlock * (2 + (2 * wide + 63) / 64); }
+constexpr size_t grad_smem(int wide) {
+    const size_t pipe = size_t(QF_GRAD_STAGES) * grad_stage(wide), red = size_t(wide) * (kGradCols + 4) * 4;
+    return (pipe > red ? pipe : red) + 1024;
 }
-template <int MT> struct GradShape {
-    static constexpr int ZS = kGradCols + 8, WS = 2 * MT * 16 + 8, RS = kGradCols + 4;
-    static constexpr size_t kPipe = size_t(kGradStages) * kGradTokens * (ZS + WS) * 2;
-    static constexpr size_t kRed = size_t(MT) * 16 * RS * sizeof(float);
-    static constexpr size_t kSmem = kPipe > kRed ? kPipe : kRed;
-};
-template <int MAXA, int MT>
-__global__ void __launch_bounds__(kGradThreads)
+template <int MAXA>
+__global__ void __launch_bounds__(kTcThreads)
 k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const uint16_t* __restrict__ x,
             int64_t ldx, int cols, const uint16_t* v, const uint16_t* __restrict__ gy, int64_t ldgy, int rows,
             const uint16_t* u, int wide_max) {
-    using S = GradShape<MT>;
-    constexpr int ZS = S::ZS, WS = S::WS, RS = S::RS;
-    extern __shared__ __align__(16) unsigned char smem[];
-    uint16_t* const zs = reinterpret_cast<uint16_t*>(smem);
-    uint16_t* const ws = zs + kGradStages * kGradTokens * ZS;
-    float* const red = reinterpret_cast<float*>(smem);
+    constexpr int RS = kGradCols + 4;
+    extern __shared__ unsigned char raw[];
+    __shared__ TcPipe<QF_GRAD_STAGES> pipe;
     wait_previous_grid();
     let_next_grid_start();
-    const int parts = gridDim.z, part = blockIdx.z, adapter = blockIdx.y;
+    const int parts = gridDim.z, part = blockIdx.z, adapter = blockIdx.y, tid = threadIdx.x;
     const Tile run = run_of(P, adapter);
     if (run.count < 0) return;                            // not this batch's plan
     const int xt = (cols + kGradCols - 1) / kGradCols;
     const bool of_a = (int)blockIdx.x < xt;
-    const uint16_t* const z = of_a ? x : gy;
-    const uint16_t* const w = of_a ? v : u;
-    const int64_t ldz = of_a ? ldx : ldgy;
     const int depth = of_a ? cols : rows, c0 = (of_a ? (int)blockIdx.x : (int)blockIdx.x - xt) * kGradCols;
-    const int rank = A.rank[adapter], wide = (rank + 15) / 16 * 16;
+    const int rank = A.rank[adapter], wide = (rank + 15) / 16 * 16, tc = tmem_cols(2 * wide);
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, stage = grad_stage(wide);
+    float* const red = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
+    pipe.start(tc);
     const int per = ((run.count + parts - 1) / parts + kGradTokens - 1) / kGradTokens * kGradTokens;
     const int first = min(run.count, part * per), last = min(run.count, first + per);
-    const int stages = (last - first + kGradTokens - 1) / kGradTokens;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-    auto fetch = [&](int s) {
-        const uint32_t zd = (uint32_t)__cvta_generic_to_shared(zs + (s % kGradStages) * kGradTokens * ZS);
-        const uint32_t wd = (uint32_t)__cvta_generic_to_shared(ws + (s % kGradStages) * kGradTokens * WS);
+    const int steps = (last - first + kGradTokens - 1) / kGradTokens;
+    if (tid < kCopiers) {
+        const uint16_t* const z = of_a ? x : gy;
+        const uint16_t* const w = of_a ? v : u;
+        const int64_t ldz = of_a ? ldx : ldgy;
+        const int chunks = wide / 4;                      // 16-byte vectors of both parts of a token
+        pipe.copy(steps, base, stage, [&](int i, uint32_t to) {
+            const int t0 = first + i * kGradTokens;
+            const int c = tid & 15;
+            const bool inside = c0 + c * 8 < depth;
 #pragma unroll
-        for (int k = 0; k < kGradTokens * 16 / kGradThreads; ++k) {
-            const int id = tid + k * kGradThreads, i = id >> 4, c = (id & 15) * 8;
-            const int t = first + s * kGradTokens + i;
-            const bool in = t < last && c0 + c < depth;
-            cp_async16(zd + (i * ZS + c) * 2, in ? z + (int64_t)run.token(t) * ldz + c0 + c : z, in);
-        }
-#pragma unroll
-        for (int k = 0; k < kGradTokens * MT * 4 / kGradThreads; ++k) {
-            const int id = tid + k * kGradThreads, i = id / (MT * 4), c = id % (MT * 4) * 8;
-            const int t = first + s * kGradTokens + i, half = c >= MT * 16, r = half ? c - MT * 16 : c;
-            const bool in = t < last && r < wide;
-            cp_async16(wd + (i * WS + c) * 2,
-                       in ? w + (int64_t)run.token(t) * 2 * wide_max + (half ? wide_max + r : r) : w, in);
-        }
-    };
-    float acc[MT][4][4] = {};
-    for (int s = 0; s < kGradStages - 1; ++s) {
-        if (s < stages) fetch(s);
-        cp_async_commit();
-    }
-    for (int s = 0; s < stages; ++s) {
-        cp_async_wait<kGradStages - 2>();
-        __syncthreads();
-        if (s + kGradStages - 1 < stages) fetch(s + kGradStages - 1);
-        cp_async_commit();
-        const uint16_t* const zd = zs + (s % kGradStages) * kGradTokens * ZS;
-        const uint16_t* const wd = ws + (s % kGradStages) * kGradTokens * WS;
-#pragma unroll
-        for (int k = 0; k < kGradTokens; k += 16) {
-            uint32_t b[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                ldmatrix_t(b[h], zd + (k + (lane & 15)) * ZS + warp * 32 + 16 * h + (lane >> 4) * 8);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (16 * m >= wide) break;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    uint32_t a[4];
-                    ldmatrix_t(a, wd + (k + (lane & 7) + ((lane >> 4) & 1) * 8) * WS + (p * MT + m) * 16 +
-                                      ((lane >> 3) & 1) * 8);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_bf16(acc[m][j], a[0], a[1], a[2], a[3], b[j / 2][2 * (j & 1)], b[j / 2][2 * (j & 1) + 1]);
-                }
+            for (int k = 0; k < 8; ++k) {
+                const int row = (tid >> 4) + 8 * k, t = t0 + row;
+                const bool in = t < last && inside;       // tokens behind the slice are zeros
+                cp_async16(to + (c >> 3) * kGradBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                           in ? z + (int64_t)run.token(t) * ldz + c0 + c * 8 : z, in);
             }
+            for (int id = tid; id < kGradTokens * chunks; id += kCopiers) {
+                const int row = id / chunks, e = id % chunks, t = t0 + row, r = e * 8;
+                const bool in = t < last;
+                cp_async16(to + (2 + (e >> 3)) * kGradBlock + row * 128 + (((e & 7) ^ (row & 7)) << 4),
+                           in ? w + (int64_t)run.token(t) * 2 * wide_max + (r < wide ? r : wide_max + r - wide) : w, in);
+            }
+        });
+    } else {
+        const uint32_t shape = mma_shape(2 * wide, true);
+        pipe.multiply(steps, base, stage, [&](int i, uint32_t from) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)                   // 16 tokens: two groups of eight rows
+                mma_tc(pipe.tmem, operand(from + 2048 * k, kGradBlock, 1024),
+                       operand(from + 2 * kGradBlock + 2048 * k, kGradBlock, 1024), shape, i > 0 || k > 0);
+        });
+    }
+    __syncthreads();
+    after_sync();
+    const bool bad = pipe.dead != 0;
+    const int warp = tid >> 5;
+    if (warp < 4) {
+        float hi[16], lo[16];
+        for (int n = 0; n < wide; n += 16) {
+            if (steps > 0) {
+                tmem_load16(pipe.tmem + (warp << 21) + n, hi);
+                tmem_load16(pipe.tmem + (warp << 21) + wide + n, lo);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) red[(n + i) * RS + tid] = steps > 0 ? hi[i] + lo[i] : 0.0f;
         }
     }
-    cp_async_wait<0>();
-    __syncthreads();
-    const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float* const at = red + (16 * m + g) * RS + warp * 32 + 8 * j + 2 * q;
-            *reinterpret_cast<float2*>(at) = make_float2(acc[m][j][0], acc[m][j][1]);
-            *reinterpret_cast<float2*>(at + 8 * RS) = make_float2(acc[m][j][2], acc[m][j][3]);
-        }
+    before_sync();
     if (parts > 1) cluster_sync(); else __syncthreads();
+    pipe.finish(tc);
     const int me = parts > 1 ? (int)cluster_rank() : 0;
     const int quads = kGradCols / 4 / parts;              // this CTA writes these columns
-    const float scale = A.scale[adapter];
-    for (int i = tid; i < rank * quads; i += kGradThreads) {
+    const float scale = bad ? __int_as_float(0x7FC00000) : A.scale[adapter];
+    for (int i = tid; i < rank * quads; i += kTcThreads) {
         const int r = of_a ? i / quads : i % rank, c = (me * quads + (of_a ? i % quads : i / rank)) * 4;
         if (c0 + c >= depth) continue;                    // depth is a multiple of 8
         const float* const at = red + r * RS + c;

@@ -94,7 +94,7 @@ def test_columns_of_one_buffer_do_not_overlap():
 def test_plan_refusals_and_sizes():
     call, size = qf.lib.qf_lora_plan, qf.lib.qf_lora_plan_bytes
     need = size(100, 3)
-    assert need == 4 * (4 + 4 + 100 + 2 * (2 + 3))
+    assert need == 4 * (4 + 4 + 100 + 2 * (1 + 3))
     assert size(-1, 3) == 0 and size(100, 0) == 0 and size(100, 513) == 0 and size((1 << 26) + 1, 1) == 0
     assert call(0x1000, 100, 0, 0x9000, need, None) == 1 and call(0x1000, 100, 513, 0x9000, need, None) == 1
     assert call(0x1000, -1, 3, 0x9000, need, None) == 2 and call(None, 100, 3, 0x9000, need, None) == 1
@@ -367,7 +367,7 @@ def test_plan_is_the_stable_sort(t, n):
     tiles = plan[5 + n + t:].view(-1, 2)[:plan[0]].tolist()                # adapter or -1, begin
     start = [0] + counts.cumsum(0).tolist()
     assert [x for x in tiles if x[0] >= 0] == [[i, start[i] + k] for i in range(n)
-                                               for k in range(0, int(counts[i]), 64)]
+                                               for k in range(0, int(counts[i]), 128)]
 
 
 @pytest.mark.gpu
