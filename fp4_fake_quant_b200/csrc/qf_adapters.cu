@@ -112,28 +112,55 @@ qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, 
     return e == cudaSuccess ? QF_OK : cuda_fail(e, "cudaLaunchKernelEx");
 }
 
-#ifndef QF_DOWN_CTAS
-#define QF_DOWN_CTAS 296        // CTAs the split of a reduction aims at
+// A [rows, width] BF16 matrix as a tensor map whose box is 64 columns of one row (the form
+// TMA gathers rows in), 128-byte swizzle, zeros outside.
+qf_status gather_map(CUtensorMap* map, const void* p, int64_t rows, int64_t width, int64_t ld) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (encode == nullptr) return fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: not found in the driver");
+    const cuuint64_t size[2] = {(cuuint64_t)width, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, 1}, step[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), size, stride, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QF_OK : fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+}
+
+#ifndef QF_DOWN_SLOTS
+#define QF_DOWN_SLOTS 3         // CTAs per SM that one wave of a split reduction may take
 #endif
-#ifndef QF_GRAD_CTAS
-#define QF_GRAD_CTAS 1184
+#ifndef QF_GRAD_SLOTS
+#define QF_GRAD_SLOTS 3
 #endif
-// Cluster size: how many CTAs share one reduction, so that `units` of them fill the GPU;
-// at most 8 (portable) and at most one per `steps` of work.
-int parts_for(int64_t units, int64_t steps, int64_t want) {
-    int p = 1;
-    while (p < 8 && units * p < want && 2 * p <= steps) p *= 2;
-    return p;
+// Cluster size: how many CTAs share one reduction.  As many as keep `units` of them within
+// one wave (a second, partial wave costs as much as a whole one), at most 8 (portable) and
+// at most one per `steps` of work.
+int parts_for(int64_t units, int64_t steps, int64_t slots) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({8, slots / std::max<int64_t>(units, 1), steps}));
 }
 
 template <int MAXA>
 qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
                int64_t depth, bool backward, void* u, int wide, bool dependent, cudaStream_t s) {
-    const int parts = parts_for(tiles, (depth + 255) / 256, QF_DOWN_CTAS);
+    CUtensorMap map{};
+    if (depth > 0) {
+        const qf_status st = gather_map(&map, z, P.tokens, depth, ldz);
+        if (st != QF_OK) return st;
+    }
+    const int parts = parts_for(tiles, (depth + 255) / 256, 148 * QF_DOWN_SLOTS);
     if (tiles * parts > INT32_MAX) return fail(QF_ERR_SHAPE, "too many tokens for one launch");
     return launch(qf::k_lora_down<MAXA>, dim3((unsigned)(tiles * parts)), qf::kTcThreads, qf::down_smem(wide), s,
-                  dependent, dim3(parts), A, P, static_cast<const uint16_t*>(z), ldz, (int)depth,
-                  (int)backward, parts, static_cast<uint16_t*>(u), wide);
+                  dependent, dim3(parts), A, P, map, (int)depth, (int)backward, parts, static_cast<uint16_t*>(u),
+                  wide);
 }
 
 template <int MAXA, int KS>
@@ -158,12 +185,21 @@ qf_status up_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, 
 template <int MAXA>
 qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf_lora_batch& c, const void* v,
                 const void* gy, int64_t ldgy, int wide, cudaStream_t s) {
+    CUtensorMap x{}, y{}, vm{}, um{};
+    qf_status st = QF_OK;
+    if (c.tokens > 0) {
+        if (c.cols > 0) st = gather_map(&x, c.x, c.tokens, c.cols, c.ldx);
+        if (st == QF_OK && c.rows > 0) st = gather_map(&y, gy, c.tokens, c.rows, ldgy);
+        if (st == QF_OK) st = gather_map(&vm, v, c.tokens, 2 * wide, 2 * wide);
+        if (st == QF_OK) st = gather_map(&um, c.u, c.tokens, 2 * wide, 2 * wide);
+        if (st != QF_OK) return st;
+    }
     const int64_t tiles = (c.cols + qf::kGradCols - 1) / qf::kGradCols + (c.rows + qf::kGradCols - 1) / qf::kGradCols;
-    const int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens, QF_GRAD_CTAS);
+    int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens, 148 * QF_GRAD_SLOTS);
+    while (parts & (parts - 1)) --parts;          // its CTAs share a tile's 128 columns evenly
     return launch(qf::k_lora_grad<MAXA>, dim3((unsigned)tiles, n, parts), qf::kTcThreads,
-                  qf::grad_smem(wide), s, true, dim3(1, 1, parts), G, P, static_cast<const uint16_t*>(c.x),
-                  c.ldx, (int)c.cols, static_cast<const uint16_t*>(v), static_cast<const uint16_t*>(gy), ldgy,
-                  (int)c.rows, static_cast<const uint16_t*>(c.u), wide);
+                  qf::grad_smem(wide), s, true, dim3(1, 1, parts), G, P, x, (int)c.cols, vm, y, (int)c.rows, um,
+                  wide);
 }
 
 template <int MAXA>

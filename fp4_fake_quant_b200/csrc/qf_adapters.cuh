@@ -10,6 +10,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 
 namespace qf {
 
@@ -312,42 +313,69 @@ __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::bef
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void writes_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// One CTA's product in TMEM: four warps copy (they gather rows, so by cp.async, 16 bytes a
-// thread, into the swizzled layout), the fifth warp's first lane issues the MMAs.  A stage
-// is full when its 128 copiers have seen their copies arrive and have fenced them for the
-// tensor core's proxy, STAGES - 1 stages after they issued them; it is empty when its MMAs
-// have committed.  FETCH(i, base) issues one thread's copies of step i; MMA(i, base) one
-// step's MMAs.  Returns false in the copiers if a wait gave up.
-constexpr int kTcThreads = 160, kCopiers = 128;
+__device__ __forceinline__ void barrier_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(smem_addr(bar)),
+                 "r"(bytes) : "memory");
+}
+// Four rows of 64 columns of a [rows, columns] BF16 matrix (the map's box is one row of 64,
+// 128-byte swizzle) to 512 bytes of shared memory; rows out of range read as zeros.
+__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int col, int4 row, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(map), "r"(col), "r"(row.x), "r"(row.y),
+                 "r"(row.z), "r"(row.w), "r"(smem_addr(bar)) : "memory");
+}
+
+// One CTA's product in TMEM.  Warp 0 gathers rows by TMA, warp 1's first lane issues the
+// MMAs, further warps may copy the other operand by cp.async; all four read the result.
+// `full` of a stage: warp 0's expected bytes and the copiers' arrivals; `empty`: its MMAs
+// have committed.
+constexpr int kTcThreads = 128;
 template <int ST>
 struct TcPipe {
     uint64_t full[ST], empty[ST], done;
     uint32_t tmem;
     int dead;
-    __device__ __forceinline__ void start(int cols) {       // every thread; ends with a barrier
+    __device__ __forceinline__ void start(int cols, int arrivals) {     // every thread; ends with a barrier
         if (threadIdx.x == 0) {
 #pragma unroll
             for (int i = 0; i < ST; ++i) {
-                barrier_init(&full[i], kCopiers);
+                barrier_init(&full[i], arrivals);
                 barrier_init(&empty[i], 1);
             }
             barrier_init(&done, 1);
             dead = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        if (threadIdx.x >= kCopiers) tmem_alloc(&tmem, cols);
+        if (threadIdx.x >> 5 == 1) tmem_alloc(&tmem, cols);
         before_sync();
         __syncthreads();
         after_sync();
     }
+    // warp 0: FETCH(i, stage base, full barrier) issues one lane's part of step i
+    template <typename FETCH>
+    __device__ __forceinline__ void gather(int steps, uint32_t base, uint32_t stage, uint32_t bytes, FETCH fetch) {
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % ST;
+            if (i >= ST && !barrier_wait(&empty[s], (i / ST - 1) & 1)) {
+                dead = 1;
+                return;
+            }
+            if (threadIdx.x == 0) barrier_expect(&full[s], bytes);
+            __syncwarp();
+            fetch(i, base + s * stage, &full[s]);
+        }
+    }
+    // copiers: FETCH(i, stage base) issues one thread's cp.async of step i; a stage's copies
+    // are waited for, and fenced for the tensor core's proxy, ST - 1 steps after their issue
     template <typename FETCH>
     __device__ __forceinline__ void copy(int steps, uint32_t base, uint32_t stage, FETCH fetch) {
-        bool ok = true;
-        for (int i = 0; i < steps + ST - 1 && ok; ++i) {
-            const int s = i % ST;
+        for (int i = 0; i < steps + ST - 1; ++i) {
             if (i < steps) {
-                if (i >= ST) ok = barrier_wait(&empty[s], (i / ST - 1) & 1);
-                if (ok) fetch(i, base + s * stage);
+                if (i >= ST && !barrier_wait(&empty[i % ST], (i / ST - 1) & 1)) {
+                    dead = 1;
+                    break;
+                }
+                fetch(i, base + (i % ST) * stage);
             }
             cp_async_commit();
             if (i >= ST - 1) {
@@ -357,41 +385,47 @@ struct TcPipe {
             }
         }
         cp_async_wait<0>();
-        if (!ok || !barrier_wait(&done, 0)) dead = 1;
     }
+    // warp 1, lane 0
     template <typename MMA>
     __device__ __forceinline__ void multiply(int steps, uint32_t base, uint32_t stage, MMA mma) {
-        if (threadIdx.x == kCopiers) {
-            for (int i = 0; i < steps; ++i) {
-                if (!barrier_wait(&full[i % ST], (i / ST) & 1)) {
-                    dead = 1;
-                    break;
-                }
-                after_sync();
-                mma(i, base + (i % ST) * stage);
-                mma_commit(&empty[i % ST]);
+        for (int i = 0; i < steps; ++i) {
+            if (!barrier_wait(&full[i % ST], (i / ST) & 1)) {
+                dead = 1;
+                break;
             }
-            mma_commit(&done);
+            after_sync();
+            mma(i, base + (i % ST) * stage);
+            mma_commit(&empty[i % ST]);
         }
+        mma_commit(&done);
     }
-    __device__ __forceinline__ void finish(int cols) {      // after a barrier of all threads
-        if (threadIdx.x >= kCopiers) tmem_free(tmem, cols);
+    __device__ __forceinline__ bool result() {              // every thread; false: a wait gave up
+        if (!barrier_wait(&done, 0)) dead = 1;
+        __syncthreads();
+        after_sync();
+        return dead == 0;
+    }
+    __device__ __forceinline__ void finish(int cols) {      // after a barrier behind the last tmem_load
+        if (threadIdx.x >> 5 == 1) tmem_free(tmem, cols);
     }
 };
 
 // ---------------------------------------------------------------- down: u = z F^T
 //
-// z [tokens, depth] (row stride ldz), F the factor with the reduction index contiguous
+// z [tokens, depth] (through its map), F the factor with the reduction index contiguous
 // ([rank, depth], row stride depth), u [tokens, 2 wide] BF16: the sums as two BF16 values,
 // the high parts first, because they are the next products' operands (one BF16 value
 // would cost the gradients as much again as their own rounding).
 // A CTA takes one tile (128 rows = the MMA's M, the rank is its N) and a slice of depth,
 // 64 columns a step; the CTAs of a cluster take the slices of one tile and add their sums
 // through distributed shared memory in rank order, so the result does not depend on timing.
-// Rows behind the tile's last are not loaded: what lies there only reaches their own rows.
+// Four of the tile's rows are one lane's TMA gather; groups of rows behind the tile's last
+// are not loaded: what lies there only reaches their own results.
 #ifndef QF_DOWN_STAGES
 #define QF_DOWN_STAGES 4
 #endif
+constexpr int kFactorCopiers = 64;
 __host__ __device__ constexpr uint32_t down_stage(int wide) { return kLoraTile * 128 + wide * 128; }
 constexpr size_t down_smem(int wide) {
     const size_t pipe = size_t(QF_DOWN_STAGES) * down_stage(wide), red = size_t(kLoraTile) * (wide + 4) * 4;
@@ -399,8 +433,8 @@ constexpr size_t down_smem(int wide) {
 }
 template <int MAXA>
 __global__ void __launch_bounds__(kTcThreads)
-k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const uint16_t* __restrict__ z,
-            int64_t ldz, int depth, int backward, int parts, uint16_t* __restrict__ u, int wide_max) {
+k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const __grid_constant__ CUtensorMap zmap,
+            int depth, int backward, int parts, uint16_t* __restrict__ u, int wide_max) {
     extern __shared__ unsigned char raw[];
     __shared__ TcPipe<QF_DOWN_STAGES> pipe;
     wait_previous_grid();
@@ -408,50 +442,46 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
     const Tile tile = tile_of(P, blockIdx.x / parts);     // parts = the cluster size
     if (tile.count <= 0) return;                         // the same for the whole cluster
     const Adapter ad = A.t[tile.adapter];
-    const int wide = (ad.rank + 15) / 16 * 16, cols = tmem_cols(wide), tid = threadIdx.x;
+    const int wide = (ad.rank + 15) / 16 * 16, cols = tmem_cols(wide);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, stage = down_stage(wide);
     float* const red = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
     const int RW = wide + 4;
-    pipe.start(cols);
+    pipe.start(cols, 1 + kFactorCopiers);
     const int steps = (depth + 63) / 64, per = (steps + parts - 1) / parts;
     const int first = min(steps, (int)(blockIdx.x % parts) * per), mine = min(steps, first + per) - first;
-    if (tid < kCopiers) {
-        const uint16_t* const f = backward ? ad.b : ad.a;
-        const int c = tid & 7, row = tid >> 3;            // 16-byte column, first of every 16th row
-        const uint32_t at = row * 128 + ((c ^ (row & 7)) << 4);
-        const uint16_t* zr[8];
+    if (warp == 0) {
+        const bool live = 4 * lane < tile.count;
+        int row[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = row + 16 * k;
-            zr[k] = i < tile.count ? z + (int64_t)tile.token(i) * ldz : nullptr;
-        }
+        for (int i = 0; i < 4; ++i) row[i] = tile.token(min(4 * lane + i, tile.count - 1));
+        pipe.gather(mine, base, stage, (tile.count + 3) / 4 * 512, [&](int i, uint32_t to, uint64_t* full) {
+            if (live) gather4(to + lane * 512, &zmap, (first + i) * 64, make_int4(row[0], row[1], row[2], row[3]), full);
+        });
+    } else if (warp == 1) {
+        const uint32_t shape = mma_shape(wide, false);
+        if (lane == 0)
+            pipe.multiply(mine, base, stage, [&](int i, uint32_t from) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_tc(pipe.tmem, operand(from + 32 * k, 16, 1024),
+                           operand(from + kLoraTile * 128 + 32 * k, 16, 1024), shape, i > 0 || k > 0);
+            });
+    } else {
+        const int c = tid & 7, r0 = (tid - 64) >> 3;      // 16-byte column, first of every 8th row
+        const uint16_t* const f = (backward ? ad.b : ad.a) + (int64_t)r0 * depth;
+        const uint32_t at = kLoraTile * 128 + r0 * 128 + ((c ^ r0) << 4);
         pipe.copy(mine, base, stage, [&](int i, uint32_t to) {
             const int k0 = (first + i) * 64 + c * 8;
-            const bool in = k0 < depth;
-            const int off = in ? k0 : 0;                  // (a zero-filled copy reads nothing)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (zr[k]) cp_async16(to + at + k * 2048, zr[k] + off, in);
-            for (int k = 0; k < wide / 16; ++k) {
-                const int r = row + 16 * k;
-                const bool live = in && r < ad.rank;
-                cp_async16(to + kLoraTile * 128 + at + k * 2048, f + (live ? (int64_t)r * depth + off : 0), live);
+            for (int k = 0; k < wide; k += 8) {
+                const bool in = k0 < depth && r0 + k < ad.rank;
+                cp_async16(to + at + k * 128, in ? f + (int64_t)k * depth + k0 : ad.a, in);
             }
         });
-    } else {
-        const uint32_t shape = mma_shape(wide, false);
-        pipe.multiply(mine, base, stage, [&](int i, uint32_t from) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_tc(pipe.tmem, operand(from + 32 * k, 16, 1024), operand(from + kLoraTile * 128 + 32 * k, 16, 1024),
-                       shape, i > 0 || k > 0);
-        });
     }
-    __syncthreads();                                      // (the copiers have seen the last MMA)
-    after_sync();
-    const bool bad = pipe.dead != 0;
-    const int warp = tid >> 5;
-    if (warp < 4 && 32 * warp < tile.count) {
+    __syncwarp();
+    const bool good = pipe.result();
+    if (32 * warp < tile.count) {
         float v[16];
         for (int n = 0; n < wide; n += 16) {
             if (mine > 0) {
@@ -472,7 +502,7 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
     for (int i = me * kTcThreads + tid; i < tile.count * quads; i += parts * kTcThreads) {
         const int t = i / quads, r = i % quads * 4;
         float4 s = parts > 1 ? sum_cluster(red + t * RW + r, parts) : *reinterpret_cast<const float4*>(red + t * RW + r);
-        if (bad) s.x = s.y = s.z = s.w = __int_as_float(0x7FC00000);
+        if (!good) s.x = s.y = s.z = s.w = __int_as_float(0x7FC00000);
         uint2 hi, lo;
         split_bf16(s, &hi, &lo);
         uint16_t* const out = u + (int64_t)tile.token(t) * 2 * wide_max + r;
@@ -647,7 +677,7 @@ struct GradTable {
 };
 constexpr int kGradCols = 128, kGradTokens = 64;
 #ifndef QF_GRAD_STAGES
-#define QF_GRAD_STAGES 4
+#define QF_GRAD_STAGES 3
 #endif
 constexpr uint32_t kGradBlock = kGradTokens * 128;         // 64 columns of a stage
 __host__ __device__ constexpr uint32_t grad_stage(int wide) { return kGradBlock * (2 + (2 * wide + 63) / 64); }
@@ -657,69 +687,67 @@ constexpr size_t grad_smem(int wide) {
 }
 template <int MAXA>
 __global__ void __launch_bounds__(kTcThreads)
-k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const uint16_t* __restrict__ x,
-            int64_t ldx, int cols, const uint16_t* v, const uint16_t* __restrict__ gy, int64_t ldgy, int rows,
-            const uint16_t* u, int wide_max) {
+k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const __grid_constant__ CUtensorMap xmap,
+            int cols, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap gymap, int rows,
+            const __grid_constant__ CUtensorMap umap, int wide_max) {
     constexpr int RS = kGradCols + 4;
     extern __shared__ unsigned char raw[];
     __shared__ TcPipe<QF_GRAD_STAGES> pipe;
     wait_previous_grid();
     let_next_grid_start();
-    const int parts = gridDim.z, part = blockIdx.z, adapter = blockIdx.y, tid = threadIdx.x;
+    const int parts = gridDim.z, part = blockIdx.z, adapter = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Tile run = run_of(P, adapter);
     if (run.count < 0) return;                            // not this batch's plan
     const int xt = (cols + kGradCols - 1) / kGradCols;
     const bool of_a = (int)blockIdx.x < xt;
     const int depth = of_a ? cols : rows, c0 = (of_a ? (int)blockIdx.x : (int)blockIdx.x - xt) * kGradCols;
-    const int rank = A.rank[adapter], wide = (rank + 15) / 16 * 16, tc = tmem_cols(2 * wide);
-    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, stage = grad_stage(wide);
+    const int rank = A.rank[adapter], wide = (rank + 15) / 16 * 16, tc = tmem_cols(2 * wide_max);
+    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, stage = grad_stage(wide_max);
     float* const red = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
-    pipe.start(tc);
+    pipe.start(tc, 1);
     const int per = ((run.count + parts - 1) / parts + kGradTokens - 1) / kGradTokens * kGradTokens;
     const int first = min(run.count, part * per), last = min(run.count, first + per);
     const int steps = (last - first + kGradTokens - 1) / kGradTokens;
-    if (tid < kCopiers) {
-        const uint16_t* const z = of_a ? x : gy;
-        const uint16_t* const w = of_a ? v : u;
-        const int64_t ldz = of_a ? ldx : ldgy;
-        const int chunks = wide / 4;                      // 16-byte vectors of both parts of a token
-        pipe.copy(steps, base, stage, [&](int i, uint32_t to) {
-            const int t0 = first + i * kGradTokens;
-            const int c = tid & 15;
-            const bool inside = c0 + c * 8 < depth;
+    if (warp == 0) {
+        // a lane's four tokens of a step; tokens behind the slice are rows out of range: zeros
+        const CUtensorMap* const zmap = of_a ? &xmap : &gymap;
+        const CUtensorMap* const wmap = of_a ? &vmap : &umap;
+        const int blocks = (2 * wide_max + 63) / 64, group = lane & 15;
+        int next[4];
+        auto ids = [&](int i) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int row = (tid >> 4) + 8 * k, t = t0 + row;
-                const bool in = t < last && inside;       // tokens behind the slice are zeros
-                cp_async16(to + (c >> 3) * kGradBlock + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                           in ? z + (int64_t)run.token(t) * ldz + c0 + c * 8 : z, in);
+            for (int k = 0; k < 4; ++k) {
+                const int t = first + i * kGradTokens + 4 * group + k;
+                next[k] = t < last ? run.token(t) : P.tokens;
             }
-            for (int id = tid; id < kGradTokens * chunks; id += kCopiers) {
-                const int row = id / chunks, e = id % chunks, t = t0 + row, r = e * 8;
-                const bool in = t < last;
-                cp_async16(to + (2 + (e >> 3)) * kGradBlock + row * 128 + (((e & 7) ^ (row & 7)) << 4),
-                           in ? w + (int64_t)run.token(t) * 2 * wide_max + (r < wide ? r : wide_max + r - wide) : w, in);
-            }
+        };
+        ids(0);
+        pipe.gather(steps, base, stage, (2 + blocks) * kGradBlock, [&](int i, uint32_t to, uint64_t* full) {
+            const int4 row = make_int4(next[0], next[1], next[2], next[3]);
+            ids(i + 1);
+            gather4(to + (lane >> 4) * kGradBlock + group * 512, zmap, c0 + (lane >> 4) * 64, row, full);
+            for (int b = lane >> 4; b < blocks; b += 2)
+                gather4(to + (2 + b) * kGradBlock + group * 512, wmap, b * 64, row, full);
         });
-    } else {
-        const uint32_t shape = mma_shape(2 * wide, true);
-        pipe.multiply(steps, base, stage, [&](int i, uint32_t from) {
+    } else if (warp == 1) {
+        const uint32_t shape = mma_shape(2 * wide_max, true);
+        if (lane == 0)
+            pipe.multiply(steps, base, stage, [&](int i, uint32_t from) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)                   // 16 tokens: two groups of eight rows
-                mma_tc(pipe.tmem, operand(from + 2048 * k, kGradBlock, 1024),
-                       operand(from + 2 * kGradBlock + 2048 * k, kGradBlock, 1024), shape, i > 0 || k > 0);
-        });
+                for (int k = 0; k < 4; ++k)               // 16 tokens: two groups of eight rows
+                    mma_tc(pipe.tmem, operand(from + 2048 * k, kGradBlock, 1024),
+                           operand(from + 2 * kGradBlock + 2048 * k, kGradBlock, 1024), shape, i > 0 || k > 0);
+            });
     }
-    __syncthreads();
-    after_sync();
-    const bool bad = pipe.dead != 0;
-    const int warp = tid >> 5;
-    if (warp < 4) {
+    __syncwarp();
+    const bool good = pipe.result();
+    {
         float hi[16], lo[16];
         for (int n = 0; n < wide; n += 16) {
             if (steps > 0) {
                 tmem_load16(pipe.tmem + (warp << 21) + n, hi);
-                tmem_load16(pipe.tmem + (warp << 21) + wide + n, lo);
+                tmem_load16(pipe.tmem + (warp << 21) + wide_max + n, lo);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) red[(n + i) * RS + tid] = steps > 0 ? hi[i] + lo[i] : 0.0f;
@@ -730,7 +758,7 @@ k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const u
     pipe.finish(tc);
     const int me = parts > 1 ? (int)cluster_rank() : 0;
     const int quads = kGradCols / 4 / parts;              // this CTA writes these columns
-    const float scale = bad ? __int_as_float(0x7FC00000) : A.scale[adapter];
+    const float scale = good ? A.scale[adapter] : __int_as_float(0x7FC00000);
     for (int i = tid; i < rank * quads; i += kTcThreads) {
         const int r = of_a ? i / quads : i % rank, c = (me * quads + (of_a ? i % quads : i / rank)) * 4;
         if (c0 + c >= depth) continue;                    // depth is a multiple of 8

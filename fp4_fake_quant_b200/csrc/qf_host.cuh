@@ -62,7 +62,14 @@ qf_status shape_of(K kernel, int threads, size_t smem, Shape* out) {
     e = cudaDeviceGetAttribute(&s.sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
     if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the limit, not this size: other launches of the kernel may need more
+        int most = 0;
+        cudaFuncAttributes fa{};
+        e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     most - (int)fa.sharedSizeBytes);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
     }
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&s.per_sm, kernel, threads, smem);
