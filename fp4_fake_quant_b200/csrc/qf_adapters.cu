@@ -112,9 +112,8 @@ qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, 
     return e == cudaSuccess ? QF_OK : cuda_fail(e, "cudaLaunchKernelEx");
 }
 
-// A [rows, width] BF16 matrix as a tensor map whose box is 64 columns of one row (the form
-// TMA gathers rows in), 128-byte swizzle, zeros outside.
-qf_status gather_map(CUtensorMap* map, const void* p, int64_t rows, int64_t width, int64_t ld) {
+// The tensor maps of a [rows, width] BF16 matrix.
+qf_status row_maps(qf::RowMaps* map, const void* p, int64_t rows, int64_t width, int64_t ld) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -128,11 +127,16 @@ qf_status gather_map(CUtensorMap* map, const void* p, int64_t rows, int64_t widt
     }();
     if (encode == nullptr) return fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: not found in the driver");
     const cuuint64_t size[2] = {(cuuint64_t)width, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, 1}, step[2] = {1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), size, stride, box, step,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? QF_OK : fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+    const cuuint32_t step[2] = {1, 1};
+    for (int i = 0; i < 2; ++i) {
+        const cuuint32_t box[2] = {64, i == 0 ? (cuuint32_t)qf::kBoxRows : 1};
+        const CUresult r = encode(i == 0 ? &map->block : &map->row, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                                  const_cast<void*>(p), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) return fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+    }
+    return QF_OK;
 }
 
 #ifndef QF_DOWN_SLOTS
@@ -151,9 +155,9 @@ int parts_for(int64_t units, int64_t steps, int64_t slots) {
 template <int MAXA>
 qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
                int64_t depth, bool backward, void* u, int wide, bool dependent, cudaStream_t s) {
-    CUtensorMap map{};
+    qf::RowMaps map{};
     if (depth > 0) {
-        const qf_status st = gather_map(&map, z, P.tokens, depth, ldz);
+        const qf_status st = row_maps(&map, z, P.tokens, depth, ldz);
         if (st != QF_OK) return st;
     }
     const int parts = parts_for(tiles, (depth + 255) / 256, 148 * QF_DOWN_SLOTS);
@@ -185,13 +189,13 @@ qf_status up_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, 
 template <int MAXA>
 qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf_lora_batch& c, const void* v,
                 const void* gy, int64_t ldgy, int wide, cudaStream_t s) {
-    CUtensorMap x{}, y{}, vm{}, um{};
+    qf::RowMaps x{}, y{}, vm{}, um{};
     qf_status st = QF_OK;
     if (c.tokens > 0) {
-        if (c.cols > 0) st = gather_map(&x, c.x, c.tokens, c.cols, c.ldx);
-        if (st == QF_OK && c.rows > 0) st = gather_map(&y, gy, c.tokens, c.rows, ldgy);
-        if (st == QF_OK) st = gather_map(&vm, v, c.tokens, 2 * wide, 2 * wide);
-        if (st == QF_OK) st = gather_map(&um, c.u, c.tokens, 2 * wide, 2 * wide);
+        if (c.cols > 0) st = row_maps(&x, c.x, c.tokens, c.cols, c.ldx);
+        if (st == QF_OK && c.rows > 0) st = row_maps(&y, gy, c.tokens, c.rows, ldgy);
+        if (st == QF_OK) st = row_maps(&vm, v, c.tokens, 2 * wide, 2 * wide);
+        if (st == QF_OK) st = row_maps(&um, c.u, c.tokens, 2 * wide, 2 * wide);
         if (st != QF_OK) return st;
     }
     const int64_t tiles = (c.cols + qf::kGradCols - 1) / qf::kGradCols + (c.rows + qf::kGradCols - 1) / qf::kGradCols;

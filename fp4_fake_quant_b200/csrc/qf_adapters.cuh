@@ -317,12 +317,22 @@ __device__ __forceinline__ void barrier_expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(smem_addr(bar)),
                  "r"(bytes) : "memory");
 }
-// Four rows of 64 columns of a [rows, columns] BF16 matrix (the map's box is one row of 64,
-// 128-byte swizzle) to 512 bytes of shared memory; rows out of range read as zeros.
-__device__ __forceinline__ void gather4(uint32_t dst, const CUtensorMap* map, int col, int4 row, uint64_t* bar) {
+// A [rows, columns] BF16 matrix for TMA, 128-byte swizzle, zeros outside: in boxes of 64
+// columns by 32 rows (rows that are neighbours), and of 64 columns of single rows, four of
+// them per gather.
+struct RowMaps {
+    CUtensorMap block, row;
+};
+constexpr int kBoxRows = 32;
+__device__ __forceinline__ void load_rows32(uint32_t dst, const RowMaps* map, int col, int row, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(&map->block), "r"(col), "r"(row), "r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void gather4(uint32_t dst, const RowMaps* map, int col, int4 row, uint64_t* bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(map), "r"(col), "r"(row.x), "r"(row.y),
-                 "r"(row.z), "r"(row.w), "r"(smem_addr(bar)) : "memory");
+                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(&map->row), "r"(col), "r"(row.x),
+                 "r"(row.y), "r"(row.z), "r"(row.w), "r"(smem_addr(bar)) : "memory");
 }
 
 // One CTA's product in TMEM.  Warp 0 gathers rows by TMA, warp 1's first lane issues the
@@ -366,10 +376,11 @@ struct TcPipe {
         }
     }
     // copiers: FETCH(i, stage base) issues one thread's cp.async of step i; a stage's copies
-    // are waited for, and fenced for the tensor core's proxy, ST - 1 steps after their issue
+    // are waited for, and fenced for the tensor core's proxy, ST - 2 steps after their issue
+    // (ST - 1 would make each MMA wait for the one before it to free a stage)
     template <typename FETCH>
     __device__ __forceinline__ void copy(int steps, uint32_t base, uint32_t stage, FETCH fetch) {
-        for (int i = 0; i < steps + ST - 1; ++i) {
+        for (int i = 0; i < steps + ST - 2; ++i) {
             if (i < steps) {
                 if (i >= ST && !barrier_wait(&empty[i % ST], (i / ST - 1) & 1)) {
                     dead = 1;
@@ -378,10 +389,10 @@ struct TcPipe {
                 fetch(i, base + (i % ST) * stage);
             }
             cp_async_commit();
-            if (i >= ST - 1) {
-                cp_async_wait<ST - 1>();
+            if (i >= ST - 2) {
+                cp_async_wait<ST - 2>();
                 writes_to_async();
-                barrier_arrive(&full[(i - (ST - 1)) % ST]);
+                barrier_arrive(&full[(i - (ST - 2)) % ST]);
             }
         }
         cp_async_wait<0>();
@@ -420,8 +431,9 @@ struct TcPipe {
 // A CTA takes one tile (128 rows = the MMA's M, the rank is its N) and a slice of depth,
 // 64 columns a step; the CTAs of a cluster take the slices of one tile and add their sums
 // through distributed shared memory in rank order, so the result does not depend on timing.
-// Four of the tile's rows are one lane's TMA gather; groups of rows behind the tile's last
-// are not loaded: what lies there only reaches their own results.
+// Tokens that are neighbours, as a request's are, come in boxes of 32 rows; others four rows
+// a gather, one per lane (a box is one instruction for what takes eight gathers, and runs
+// at twice their rate).  Rows behind the tile's last only reach their own results.
 #ifndef QF_DOWN_STAGES
 #define QF_DOWN_STAGES 4
 #endif
@@ -433,7 +445,7 @@ constexpr size_t down_smem(int wide) {
 }
 template <int MAXA>
 __global__ void __launch_bounds__(kTcThreads)
-k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const __grid_constant__ CUtensorMap zmap,
+k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const __grid_constant__ RowMaps zmap,
             int depth, int backward, int parts, uint16_t* __restrict__ u, int wide_max) {
     extern __shared__ unsigned char raw[];
     __shared__ TcPipe<QF_DOWN_STAGES> pipe;
@@ -451,12 +463,22 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
     const int steps = (depth + 63) / 64, per = (steps + parts - 1) / parts;
     const int first = min(steps, (int)(blockIdx.x % parts) * per), mine = min(steps, first + per) - first;
     if (warp == 0) {
-        const bool live = 4 * lane < tile.count;
+        const int b = lane >> 3;                          // eight lanes to a box of 32 rows
         int row[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) row[i] = tile.token(min(4 * lane + i, tile.count - 1));
-        pipe.gather(mine, base, stage, (tile.count + 3) / 4 * 512, [&](int i, uint32_t to, uint64_t* full) {
-            if (live) gather4(to + lane * 512, &zmap, (first + i) * 64, make_int4(row[0], row[1], row[2], row[3]), full);
+        const int live = min(kBoxRows, tile.count - b * kBoxRows);
+        const int top = __shfl_sync(0xFFFFFFFFu, row[0], lane & 24);
+        const int end = live > 0 ? tile.token(b * kBoxRows + live - 1) : 0;
+        const bool dense = live > 0 && end - top == live - 1;           // (the plan keeps tokens in order)
+        pipe.gather(mine, base, stage, (tile.count + kBoxRows - 1) / kBoxRows * kBoxRows * 128,
+                    [&](int i, uint32_t to, uint64_t* full) {
+            const int col = (first + i) * 64;
+            if (dense) {
+                if ((lane & 7) == 0) load_rows32(to + b * kBoxRows * 128, &zmap, col, top, full);
+            } else if (live > 0) {
+                gather4(to + lane * 512, &zmap, col, make_int4(row[0], row[1], row[2], row[3]), full);
+            }
         });
     } else if (warp == 1) {
         const uint32_t shape = mma_shape(wide, false);
@@ -687,9 +709,9 @@ constexpr size_t grad_smem(int wide) {
 }
 template <int MAXA>
 __global__ void __launch_bounds__(kTcThreads)
-k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const __grid_constant__ CUtensorMap xmap,
-            int cols, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap gymap, int rows,
-            const __grid_constant__ CUtensorMap umap, int wide_max) {
+k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const __grid_constant__ RowMaps xmap,
+            int cols, const __grid_constant__ RowMaps vmap, const __grid_constant__ RowMaps gymap, int rows,
+            const __grid_constant__ RowMaps umap, int wide_max) {
     constexpr int RS = kGradCols + 4;
     extern __shared__ unsigned char raw[];
     __shared__ TcPipe<QF_GRAD_STAGES> pipe;
@@ -710,25 +732,41 @@ k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const _
     const int first = min(run.count, part * per), last = min(run.count, first + per);
     const int steps = (last - first + kGradTokens - 1) / kGradTokens;
     if (warp == 0) {
-        // a lane's four tokens of a step; tokens behind the slice are rows out of range: zeros
-        const CUtensorMap* const zmap = of_a ? &xmap : &gymap;
-        const CUtensorMap* const wmap = of_a ? &vmap : &umap;
-        const int blocks = (2 * wide_max + 63) / 64, group = lane & 15;
+        // a step's 64 tokens: two boxes per 64 columns where they are neighbours; otherwise
+        // sixteen gathers (tokens behind the slice as rows out of range: zeros)
+        const RowMaps* const zmap = of_a ? &xmap : &gymap;
+        const RowMaps* const wmap = of_a ? &vmap : &umap;
+        const int blocks = 2 + (2 * wide_max + 63) / 64;       // of 64 columns: two of z, then w's
         int next[4];
-        auto ids = [&](int i) {
+        auto ids = [&](int i) {                                // a lane's four tokens of a step
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int t = first + i * kGradTokens + 4 * group + k;
+                const int t = first + i * kGradTokens + 4 * (lane & 15) + k;
                 next[k] = t < last ? run.token(t) : P.tokens;
             }
         };
         ids(0);
-        pipe.gather(steps, base, stage, (2 + blocks) * kGradBlock, [&](int i, uint32_t to, uint64_t* full) {
+        pipe.gather(steps, base, stage, blocks * kGradBlock, [&](int i, uint32_t to, uint64_t* full) {
             const int4 row = make_int4(next[0], next[1], next[2], next[3]);
             ids(i + 1);
-            gather4(to + (lane >> 4) * kGradBlock + group * 512, zmap, c0 + (lane >> 4) * 64, row, full);
-            for (int b = lane >> 4; b < blocks; b += 2)
-                gather4(to + (2 + b) * kGradBlock + group * 512, wmap, b * 64, row, full);
+            // each half of the step's tokens by itself; both halves of the warp hold all of them
+            int top[2];
+            bool dense[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                top[h] = __shfl_sync(0xFFFFFFFFu, row.x, 8 * h);
+                dense[h] = __shfl_sync(0xFFFFFFFFu, row.w, 8 * h + 7) - top[h] == kBoxRows - 1 &&
+                           first + i * kGradTokens + (h + 1) * kBoxRows <= last;
+            }
+            const int mine = lane >> 3 & 1;
+            for (int b = lane >> 4; b < blocks; b += 2) {
+                const RowMaps* const map = b < 2 ? zmap : wmap;
+                const int col = b < 2 ? c0 + b * 64 : (b - 2) * 64;
+                if (!dense[mine])
+                    gather4(to + b * kGradBlock + (lane & 15) * 512, map, col, row, full);
+                else if ((lane & 7) == 0)
+                    load_rows32(to + b * kGradBlock + mine * kBoxRows * 128, map, col, top[mine], full);
+            }
         });
     } else if (warp == 1) {
         const uint32_t shape = mma_shape(2 * wide_max, true);
