@@ -428,9 +428,9 @@ struct TcPipe {
 // ([rank, depth], row stride depth), u [tokens, 2 wide] BF16: the sums as two BF16 values,
 // the high parts first, because they are the next products' operands (one BF16 value
 // would cost the gradients as much again as their own rounding).
-// A CTA takes one tile (128 rows = the MMA's M, the rank is its N) and a slice of depth,
-// 64 columns a step; the CTAs of a cluster take the slices of one tile and add their sums
-// through distributed shared memory in rank order, so the result does not depend on timing.
+// A CTA takes one tile (128 rows = the MMA's M, the rank is its N) and steps of 64 columns of
+// depth; the CTAs of a cluster share one tile's steps and add their sums through
+// distributed shared memory in rank order, so the result does not depend on timing.
 // Tokens that are neighbours, as a request's are, come in boxes of 32 rows; others four rows
 // a gather, one per lane (a box is one instruction for what takes eight gathers, and runs
 // at twice their rate).  Rows behind the tile's last only reach their own results.
@@ -460,8 +460,8 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
     float* const red = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
     const int RW = wide + 4;
     pipe.start(cols, 1 + kFactorCopiers);
-    const int steps = (depth + 63) / 64, per = (steps + parts - 1) / parts;
-    const int first = min(steps, (int)(blockIdx.x % parts) * per), mine = min(steps, first + per) - first;
+    // a cluster's CTAs take every parts-th step: together they read whole stretches of a row
+    const int part = blockIdx.x % parts, mine = ((depth + 63) / 64 - part + parts - 1) / parts;
     if (warp == 0) {
         const int b = lane >> 3;                          // eight lanes to a box of 32 rows
         int row[4];
@@ -473,7 +473,7 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
         const bool dense = live > 0 && end - top == live - 1;           // (the plan keeps tokens in order)
         pipe.gather(mine, base, stage, (tile.count + kBoxRows - 1) / kBoxRows * kBoxRows * 128,
                     [&](int i, uint32_t to, uint64_t* full) {
-            const int col = (first + i) * 64;
+            const int col = (part + i * parts) * 64;
             if (dense) {
                 if ((lane & 7) == 0) load_rows32(to + b * kBoxRows * 128, &zmap, col, top, full);
             } else if (live > 0) {
@@ -494,7 +494,7 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
         const uint16_t* const f = (backward ? ad.b : ad.a) + (int64_t)r0 * depth;
         const uint32_t at = kLoraTile * 128 + r0 * 128 + ((c ^ r0) << 4);
         pipe.copy(mine, base, stage, [&](int i, uint32_t to) {
-            const int k0 = (first + i) * 64 + c * 8;
+            const int k0 = (part + i * parts) * 64 + c * 8;
             for (int k = 0; k < wide; k += 8) {
                 const bool in = k0 < depth && r0 + k < ad.rank;
                 cp_async16(to + at + k * 128, in ? f + (int64_t)k * depth + k0 : ad.a, in);
