@@ -17,7 +17,6 @@ using qf::AdapterTable;
 using qf::PlanView;
 using qf::kLoraMaxAdapters;
 using qf::kLoraMaxRank;
-using qf::kLoraThreads;
 using qf::kLoraTile;
 
 constexpr int kSmallA = 8, kMidA = 64, kLargeA = kLoraMaxAdapters;   // descriptor table sizes
@@ -168,22 +167,21 @@ qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, co
 }
 
 template <int MAXA, int KS>
-qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide,
-             int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
-    const int64_t blocks = tiles * (kLoraTile / qf::kUpTile) * ((width + 255) / 256);
+qf_status up_ks(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide,
+                int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
+    const int64_t blocks = tiles * ((width + 255) / 256);
     if (blocks > INT32_MAX) return fail(QF_ERR_SHAPE, "tokens x width too large for one launch");
-    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), kLoraThreads,
-                  qf::UpShape<KS>::kSmem, s, true, dim3(1), A, P,
-                  static_cast<const uint16_t*>(u), wide, (int)width, (int)backward,
+    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), qf::kUpThreads, qf::UpShape<KS>::kSmem, s, true,
+                  dim3(1), A, P, static_cast<const uint16_t*>(u), wide, (int)width, (int)backward,
                   static_cast<uint16_t*>(y), ldy);
 }
 template <int MAXA>
-qf_status up_any(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide,
-                 int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
-    if (wide <= 16) return up<MAXA, 1>(A, P, tiles, u, wide, width, backward, y, ldy, s);
-    if (wide <= 32) return up<MAXA, 2>(A, P, tiles, u, wide, width, backward, y, ldy, s);
-    if (wide <= 64) return up<MAXA, 4>(A, P, tiles, u, wide, width, backward, y, ldy, s);
-    return up<MAXA, 8>(A, P, tiles, u, wide, width, backward, y, ldy, s);
+qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide, int64_t width,
+             bool backward, void* y, int64_t ldy, cudaStream_t s) {
+    if (wide <= 16) return up_ks<MAXA, 1>(A, P, tiles, u, wide, width, backward, y, ldy, s);
+    if (wide <= 32) return up_ks<MAXA, 2>(A, P, tiles, u, wide, width, backward, y, ldy, s);
+    if (wide <= 64) return up_ks<MAXA, 4>(A, P, tiles, u, wide, width, backward, y, ldy, s);
+    return up_ks<MAXA, 8>(A, P, tiles, u, wide, width, backward, y, ldy, s);
 }
 
 template <int MAXA>
@@ -228,7 +226,7 @@ qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int wide, cudaS
     const int64_t tiles = tiles_of(c, n);
     qf_status st = down<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, wide, false, s);
     if (st != QF_OK || c.rows == 0) return st;
-    return up_any<MAXA>(A, P, tiles, c.u, wide, c.rows, false, c.y, c.ldy, s);
+    return up<MAXA>(A, P, tiles, c.u, wide, c.rows, false, c.y, c.ldy, s);
 }
 
 int64_t aligned(int64_t bytes) { return (bytes + 255) / 256 * 256; }
@@ -264,7 +262,7 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
         st = down<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, wide, true, s);
         if (st != QF_OK) return st;
         if (gx && c.cols > 0) {
-            st = up_any<MAXA>(A, P, tiles, v, wide, c.cols, true, gx, ldgx, s);
+            st = up<MAXA>(A, P, tiles, v, wide, c.cols, true, gx, ldgx, s);
             if (st != QF_OK) return st;
         }
     }

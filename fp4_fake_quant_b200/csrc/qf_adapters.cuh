@@ -17,7 +17,6 @@ namespace qf {
 constexpr int kLoraTile = 128;          // tokens of one tile (all of one adapter)
 constexpr int kLoraMaxAdapters = 512;
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanHead = 4;            // words: tiles, tokens with an adapter, tokens, adapters
 
@@ -176,12 +175,15 @@ __device__ __forceinline__ Tile run_of(const PlanView& P, int adapter) {   // an
     return t;
 }
 
-__device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
                  "{%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix(uint32_t* r, uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 __device__ __forceinline__ uint32_t bf16x2(float hi, float lo) {
     uint32_t r;
@@ -235,11 +237,6 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t at) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
     return v;
 }
 
@@ -375,12 +372,12 @@ struct TcPipe {
             fetch(i, base + s * stage, &full[s]);
         }
     }
-    // copiers: FETCH(i, stage base) issues one thread's cp.async of step i; a stage's copies
-    // are waited for, and fenced for the tensor core's proxy, ST - 2 steps after their issue
-    // (ST - 1 would make each MMA wait for the one before it to free a stage)
+    // copiers: FETCH(i, stage base) issues one thread's cp.async of step i; a step's copies
+    // are waited for, and fenced for the tensor core's proxy, one step later (the later, the
+    // closer each MMA comes to waiting for those before it to free a stage)
     template <typename FETCH>
     __device__ __forceinline__ void copy(int steps, uint32_t base, uint32_t stage, FETCH fetch) {
-        for (int i = 0; i < steps + ST - 2; ++i) {
+        for (int i = 0; i < steps + 1; ++i) {
             if (i < steps) {
                 if (i >= ST && !barrier_wait(&empty[i % ST], (i / ST - 1) & 1)) {
                     dead = 1;
@@ -389,10 +386,10 @@ struct TcPipe {
                 fetch(i, base + (i % ST) * stage);
             }
             cp_async_commit();
-            if (i >= ST - 2) {
-                cp_async_wait<ST - 2>();
+            if (i >= 1) {
+                cp_async_wait<1>();
                 writes_to_async();
-                barrier_arrive(&full[(i - (ST - 2)) % ST]);
+                barrier_arrive(&full[(i - 1) % ST]);
             }
         }
         cp_async_wait<0>();
@@ -538,80 +535,84 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
 //
 // u [tokens, 2 wide_max] (high and low parts), F [width, ldf] with the rank contiguous
 // (forward: B itself, ldf = rank; backward: A^T, padded), y [tokens, width] BF16 (row
-// stride ldy), read, added to in FP32 and rounded once.  A warp owns 32 columns and keeps
-// their factor rows as fragments; the columns are dealt to the four 8-wide MMA tiles so
-// that a lane ends up with 8 neighbouring columns of its rows: y moves in 16-byte vectors,
-// 64 bytes per row.  All of the tile's y is on its way (cp.async, each lane what it will
-// read itself) before the first product; u comes once per CTA.
+// stride ldy), read, added to in FP32 and rounded once.  Twice the bytes of the reductions
+// above for half the products: mma.sync keeps up here, and its accumulators lie in the
+// registers of the lanes that own y (tcgen05 with y tiles through shared memory and TMEM
+// took 95 us where this form takes 82).  A warp owns 32 columns of the tile's tokens and
+// keeps their factor rows as fragments; the columns are dealt to the four 8-wide MMA tiles
+// so that a lane ends up with 8 neighbouring columns of its rows: y moves in 16-byte
+// vectors, 64 bytes per row, four groups of 16 tokens ahead (cp.async, each lane exactly
+// what it will read itself, so without barriers).  u comes once per CTA.
 // KS: 16-deep rank steps.
-constexpr int kUpTile = 64;             // tokens of one CTA: half a tile
+constexpr int kUpThreads = 256, kUpAhead = 4;
 template <int KS> struct UpShape {
     static constexpr int kRow = 2 * KS * 16 + 8;          // u's row in shared memory, padded
-    static constexpr size_t kSmem = size_t(kUpTile) * kRow * 2 + size_t(8) * 8 * 512;
+    static constexpr size_t kU = size_t(kLoraTile) * kRow * 2;
+    static constexpr size_t kSmem = kU + size_t(8) * kUpAhead * 2 * 512;
 };
 template <int MAXA, int KS>
-__global__ void __launch_bounds__(kLoraThreads)
+__global__ void __launch_bounds__(kUpThreads)
 k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const uint16_t* u, int wide_max,
           int width, int backward, uint16_t* __restrict__ y, int64_t ldy) {
     constexpr int UR = UpShape<KS>::kRow;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ int token[kLoraTile];
     wait_previous_grid();
     let_next_grid_start();
     const int across = (width + 255) / 256;
-    Tile tile = tile_of(P, blockIdx.x / across / 2);
-    const int part = blockIdx.x / across % 2 * kUpTile;
-    tile.begin += part;
-    tile.count = min(tile.count - part, kUpTile);
+    const Tile tile = tile_of(P, blockIdx.x / across);
     if (tile.count <= 0) return;
     const Adapter ad = A.t[tile.adapter];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const int n0 = (int)(blockIdx.x % across) * 256 + warp * 32, col = n0 + 8 * q;
     const int ks = (ad.rank + 15) / 16;
-    const uint32_t us = (uint32_t)__cvta_generic_to_shared(smem);
-    const uint32_t ys = us + kUpTile * UR * 2 + warp * 8 * 512 + lane * 16;
-    for (int i = threadIdx.x; i < tile.count * ks * 4; i += kLoraThreads) {
+    const uint32_t us = smem_addr(raw), ys = us + (uint32_t)UpShape<KS>::kU + warp * kUpAhead * 1024 + lane * 16;
+    if (tid < kLoraTile) token[tid] = tile.token(min(tid, tile.count - 1));
+    __syncthreads();
+    for (int i = tid; i < tile.count * ks * 4; i += kUpThreads) {
         const int t = i / (ks * 4), c = i % (ks * 4) * 8;          // high parts, then low parts
-        const int half = c >= ks * 16;
-        cp_async16(us + (t * UR + (half ? KS * 16 + c - ks * 16 : c)) * 2,
-                   u + (int64_t)tile.token(t) * 2 * wide_max + (half ? wide_max + c - ks * 16 : c), true);
+        const bool low = c >= ks * 16;
+        cp_async16(us + (t * UR + (low ? KS * 16 + c - ks * 16 : c)) * 2,
+                   u + (int64_t)token[t] * 2 * wide_max + (low ? wide_max + c - ks * 16 : c), true);
     }
     cp_async_commit();
-    uint16_t* at[4][2];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    uint16_t* const ycol = y + col;
+    const bool inside = col < width;
+    auto fetch = [&](int m) {                              // 16 tokens: this lane's two rows
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = 16 * m + 8 * h + g;
-            const bool in = i < tile.count && col < width;
-            at[m][h] = in ? y + (int64_t)tile.token(i) * ldy + col : nullptr;
-            if (in) cp_async16(ys + (2 * m + h) * 512, at[m][h], true);
+            if (inside && i < tile.count)
+                cp_async16(ys + ((m % kUpAhead) * 2 + h) * 512, ycol + (int64_t)token[i] * ldy, true);
         }
         cp_async_commit();
-    }
-    uint2 fv[KS][4];
+    };
+#pragma unroll
+    for (int m = 0; m < kUpAhead; ++m) fetch(m);
+    uint32_t fv[KS][4][2];
     const uint16_t* const f = backward ? ad.a : ad.b;
     const int ldf = backward ? ks * 16 : ad.rank;
-    const bool vec = (ldf & 3) == 0 && (reinterpret_cast<uintptr_t>(f) & 7) == 0;
+    const bool vec = (ldf & 1) == 0 && (reinterpret_cast<uintptr_t>(f) & 3) == 0;
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
+    for (int j = 0; j < 4; ++j) {
+        const int c = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
+        const uint16_t* const p = f + (int64_t)c * ldf + 2 * q;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = n0 + 8 * (g >> 1) + 2 * j + (g & 1), r = 16 * k + 4 * q;
-            const uint16_t* const p = f + (int64_t)c * ldf + r;
-            fv[k][j] = make_uint2(0, 0);
-            if (c >= width || r >= ldf) continue;
-            if (vec) {
-                fv[k][j] = *reinterpret_cast<const uint2*>(p);
-            } else {
-                fv[k][j].x = p[0] | (r + 1 < ldf ? (uint32_t)p[1] << 16 : 0u);
-                if (r + 2 < ldf) fv[k][j].y = p[2] | (r + 3 < ldf ? (uint32_t)p[3] << 16 : 0u);
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 16 * k + 8 * h;
+                fv[k][j][h] = 0;
+                if (c >= width || r + 2 * q >= ldf) continue;
+                if (vec) fv[k][j][h] = *reinterpret_cast<const uint32_t*>(p + r);
+                else fv[k][j][h] = p[r] | (r + 2 * q + 1 < ldf ? (uint32_t)p[r + 1] << 16 : 0u);
             }
-        }
-    cp_async_wait<4>();
+    }
+    cp_async_wait<kUpAhead>();
     __syncthreads();                                       // u is there for every warp
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        if (16 * m >= tile.count) break;
+    const uint32_t ua = us + (((lane & 15) * UR) + (lane >> 4) * 8) * 2;
+    const int groups = (tile.count + 15) / 16;
+    for (int m = 0; m < groups; ++m) {
         float acc[4][4] = {};
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -619,26 +620,25 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
             for (int k = 0; k < KS; ++k) {
                 if (k >= ks) break;
                 // rows behind the tile are stale shared memory: their products are not used
-                const uint32_t up = us + ((16 * m + g) * UR + p * KS * 16 + 16 * k + 4 * q) * 2;
-                const uint2 u0 = lds8(up), u1 = lds8(up + 8 * UR * 2);
+                uint32_t a[4];
+                ldmatrix(a, ua + (16 * m * UR + p * KS * 16 + 16 * k) * 2);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma_bf16(acc[j], u0.x, u1.x, u0.y, u1.y, fv[k][j].x, fv[k][j].y);
+                for (int j = 0; j < 4; ++j) mma_bf16(acc[j], a, fv[k][j][0], fv[k][j][1]);
             }
-        if (m == 0) cp_async_wait<3>();
-        if (m == 1) cp_async_wait<2>();
-        if (m == 2) cp_async_wait<1>();
-        if (m == 3) cp_async_wait<0>();
+        cp_async_wait<kUpAhead - 1>();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (!at[m][h]) continue;
-            const uint4 yv = lds16(ys + (2 * m + h) * 512);
-            uint32_t w[4] = {yv.x, yv.y, yv.z, yv.w};
+            const int i = 16 * m + 8 * h + g;
+            if (!inside || i >= tile.count) continue;
+            const uint4 v = lds16(ys + ((m % kUpAhead) * 2 + h) * 512);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                w[j] = bf16x2(__uint_as_float(w[j] & 0xFFFF0000u) + ad.scale * acc[j][2 * h + 1],
-                              __uint_as_float(w[j] << 16) + ad.scale * acc[j][2 * h]);
-            *reinterpret_cast<uint4*>(at[m][h]) = make_uint4(w[0], w[1], w[2], w[3]);
+                w[j] = bf16x2(__fmaf_rn(ad.scale, acc[j][2 * h + 1], __uint_as_float(w[j] & 0xFFFF0000u)),
+                              __fmaf_rn(ad.scale, acc[j][2 * h], __uint_as_float(w[j] << 16)));
+            *reinterpret_cast<uint4*>(ycol + (int64_t)token[i] * ldy) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        fetch(m + kUpAhead);
     }
     cp_async_wait<0>();
 }
