@@ -171,7 +171,8 @@ qf_status up_ks(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, c
                 int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
     const int64_t blocks = tiles * ((width + 255) / 256);
     if (blocks > INT32_MAX) return fail(QF_ERR_SHAPE, "tokens x width too large for one launch");
-    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), qf::kUpThreads, qf::UpShape<KS>::kSmem, s, true,
+    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), qf::kUpThreads,
+                  qf::UpShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16)), s, true,
                   dim3(1), A, P, static_cast<const uint16_t*>(u), wide, (int)width, (int)backward,
                   static_cast<uint16_t*>(y), ldy);
 }
@@ -218,12 +219,27 @@ int64_t tiles_of(const qf_lora_batch& c, int n) {
     return c.d_plan ? qf::plan_tiles(c.tokens, n) : (c.tokens + kLoraTile - 1) / kLoraTile;
 }
 
+template <int MAXA, int KS>
+qf_status few(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const qf_lora_batch& c, int wide,
+              cudaStream_t s) {
+    return launch(qf::k_lora_few<MAXA, KS>, dim3((unsigned)tiles * qf::kFewParts), qf::kUpThreads,
+                  qf::FewShape<KS>::kSmem, s, false, dim3(qf::kFewParts), A, P, static_cast<const uint16_t*>(c.x),
+                  c.ldx, (int)c.cols, static_cast<uint16_t*>(c.u), wide, (int)c.rows, static_cast<uint16_t*>(c.y),
+                  c.ldy);
+}
+
 template <int MAXA>
 qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int wide, cudaStream_t s) {
     AdapterTable<MAXA> A;
     fill(A, l, n);
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
+    if (c.tokens <= qf::kFewTokens) {
+        if (wide <= 16) return few<MAXA, 1>(A, P, tiles, c, wide, s);
+        if (wide <= 32) return few<MAXA, 2>(A, P, tiles, c, wide, s);
+        if (wide <= 64) return few<MAXA, 4>(A, P, tiles, c, wide, s);
+        return few<MAXA, 8>(A, P, tiles, c, wide, s);
+    }
     qf_status st = down<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, wide, false, s);
     if (st != QF_OK || c.rows == 0) return st;
     return up<MAXA>(A, P, tiles, c.u, wide, c.rows, false, c.y, c.ldy, s);

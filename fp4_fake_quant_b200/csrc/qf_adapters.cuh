@@ -547,42 +547,24 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
 constexpr int kUpThreads = 256, kUpAhead = 4;
 template <int KS> struct UpShape {
     static constexpr int kRow = 2 * KS * 16 + 8;          // u's row in shared memory, padded
-    static constexpr size_t kU = size_t(kLoraTile) * kRow * 2;
-    static constexpr size_t kSmem = kU + size_t(8) * kUpAhead * 2 * 512;
+    static constexpr size_t kRing = size_t(8) * kUpAhead * 2 * 512;
+    __host__ __device__ static constexpr size_t u_bytes(int tokens) { return size_t(tokens) * kRow * 2; }
+    __host__ __device__ static constexpr size_t smem(int tokens) { return u_bytes(tokens) + kRing; }
 };
-template <int MAXA, int KS>
-__global__ void __launch_bounds__(kUpThreads)
-k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const uint16_t* u, int wide_max,
-          int width, int backward, uint16_t* __restrict__ y, int64_t ldy) {
+// A warp's 32 columns from n0 on.  us: u in shared memory ([tokens rounded up to 16][kRow]);
+// ys: this lane's part of the ring; ready(): called once, before u is read.
+template <int KS, typename READY>
+__device__ __forceinline__ void up_columns(const Adapter& ad, int backward, int count, const int* token, uint32_t us,
+                                           uint32_t ys, int n0, int width, uint16_t* y, int64_t ldy, READY ready) {
     constexpr int UR = UpShape<KS>::kRow;
-    extern __shared__ __align__(16) unsigned char raw[];
-    __shared__ int token[kLoraTile];
-    wait_previous_grid();
-    let_next_grid_start();
-    const int across = (width + 255) / 256;
-    const Tile tile = tile_of(P, blockIdx.x / across);
-    if (tile.count <= 0) return;
-    const Adapter ad = A.t[tile.adapter];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    const int n0 = (int)(blockIdx.x % across) * 256 + warp * 32, col = n0 + 8 * q;
-    const int ks = (ad.rank + 15) / 16;
-    const uint32_t us = smem_addr(raw), ys = us + (uint32_t)UpShape<KS>::kU + warp * kUpAhead * 1024 + lane * 16;
-    if (tid < kLoraTile) token[tid] = tile.token(min(tid, tile.count - 1));
-    __syncthreads();
-    for (int i = tid; i < tile.count * ks * 4; i += kUpThreads) {
-        const int t = i / (ks * 4), c = i % (ks * 4) * 8;          // high parts, then low parts
-        const bool low = c >= ks * 16;
-        cp_async16(us + (t * UR + (low ? KS * 16 + c - ks * 16 : c)) * 2,
-                   u + (int64_t)token[t] * 2 * wide_max + (low ? wide_max + c - ks * 16 : c), true);
-    }
-    cp_async_commit();
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, col = n0 + 8 * q, ks = (ad.rank + 15) / 16;
     uint16_t* const ycol = y + col;
     const bool inside = col < width;
     auto fetch = [&](int m) {                              // 16 tokens: this lane's two rows
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = 16 * m + 8 * h + g;
-            if (inside && i < tile.count)
+            if (inside && i < count)
                 cp_async16(ys + ((m % kUpAhead) * 2 + h) * 512, ycol + (int64_t)token[i] * ldy, true);
         }
         cp_async_commit();
@@ -608,10 +590,9 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
                 else fv[k][j][h] = p[r] | (r + 2 * q + 1 < ldf ? (uint32_t)p[r + 1] << 16 : 0u);
             }
     }
-    cp_async_wait<kUpAhead>();
-    __syncthreads();                                       // u is there for every warp
+    ready();
     const uint32_t ua = us + (((lane & 15) * UR) + (lane >> 4) * 8) * 2;
-    const int groups = (tile.count + 15) / 16;
+    const int groups = (count + 15) / 16;
     for (int m = 0; m < groups; ++m) {
         float acc[4][4] = {};
 #pragma unroll
@@ -629,7 +610,7 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = 16 * m + 8 * h + g;
-            if (!inside || i >= tile.count) continue;
+            if (!inside || i >= count) continue;
             const uint4 v = lds16(ys + ((m % kUpAhead) * 2 + h) * 512);
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -641,6 +622,145 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
         fetch(m + kUpAhead);
     }
     cp_async_wait<0>();
+}
+
+template <int MAXA, int KS>
+__global__ void __launch_bounds__(kUpThreads)
+k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const uint16_t* u, int wide_max,
+          int width, int backward, uint16_t* y, int64_t ldy) {
+    constexpr int UR = UpShape<KS>::kRow;
+    extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ int token[kLoraTile];
+    wait_previous_grid();
+    let_next_grid_start();
+    const int across = (width + 255) / 256;
+    const Tile tile = tile_of(P, blockIdx.x / across);
+    if (tile.count <= 0) return;
+    const Adapter ad = A.t[tile.adapter];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ks = (ad.rank + 15) / 16, rows = min(kLoraTile, (P.tokens + 15) / 16 * 16);
+    const uint32_t us = smem_addr(raw);
+    const uint32_t ys = us + (uint32_t)UpShape<KS>::u_bytes(rows) + warp * kUpAhead * 1024 + lane * 16;
+    if (tid < kLoraTile) token[tid] = tile.token(min(tid, tile.count - 1));
+    __syncthreads();
+    for (int i = tid; i < tile.count * ks * 4; i += kUpThreads) {
+        const int t = i / (ks * 4), c = i % (ks * 4) * 8;          // high parts, then low parts
+        const bool low = c >= ks * 16;
+        cp_async16(us + (t * UR + (low ? KS * 16 + c - ks * 16 : c)) * 2,
+                   u + (int64_t)token[t] * 2 * wide_max + (low ? wide_max + c - ks * 16 : c), true);
+    }
+    cp_async_commit();
+    up_columns<KS>(ad, backward, tile.count, token, us, ys, (int)(blockIdx.x % across) * 256 + warp * 32, width, y, ldy,
+                   [] {
+                       cp_async_wait<kUpAhead>();
+                       __syncthreads();                    // u is there for every warp
+                   });
+}
+
+// ---------------------------------------------------------------- few tokens: down and up in one launch
+//
+// Decoding batches: a handful of tokens per adapter, so the factors are most of the bytes
+// and launches and waits most of the time.  A cluster of eight CTAs takes one tile: each
+// forms its eighth of the depth (mma.sync straight from registers: the 16 bytes a lane
+// loads are its fragments, with the reduction index permuted alike on both operands), all
+// of them add the eight parts through distributed shared memory, each then does its eighth
+// of the columns.  The slice of B is on its way to L2 meanwhile.
+constexpr int kFewParts = 8, kFewTokens = 64;
+template <int KS> struct FewShape {
+    static constexpr int kSum = KS * 16 + 4;              // floats per token of a partial u
+    static constexpr size_t kPart = size_t(8) * 16 * kSum * 4;      // a warp's 16 tokens each
+    static constexpr size_t kAll = size_t(kFewTokens) * kSum * 4;   // the CTA's
+    static constexpr size_t kWork = kPart > UpShape<KS>::smem(kFewTokens) ? kPart : UpShape<KS>::smem(kFewTokens);
+    static constexpr size_t kSmem = kAll + kWork;
+};
+template <int MAXA, int KS>
+__global__ void __launch_bounds__(kUpThreads)
+k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const uint16_t* __restrict__ x, int64_t ldx,
+           int cols, uint16_t* __restrict__ u, int wide_max, int rows, uint16_t* y, int64_t ldy) {
+    constexpr int SR = FewShape<KS>::kSum, UR = UpShape<KS>::kRow, NT = KS * 2;
+    extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ int token[kFewTokens];
+    float* const all = reinterpret_cast<float*>(raw);
+    float* const part = reinterpret_cast<float*>(raw + FewShape<KS>::kAll);
+    const Tile tile = tile_of(P, blockIdx.x / kFewParts);
+    if (tile.count <= 0) return;                          // the same for the whole cluster
+    const Adapter ad = A.t[tile.adapter];
+    const int me = blockIdx.x % kFewParts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, q = lane & 3, wide = (ad.rank + 15) / 16 * 16;
+    // this CTA's columns of y: whole 32-column groups, shared out evenly
+    const int per = ((rows + 31) / 32 + kFewParts - 1) / kFewParts * 32, n0 = me * per, n1 = min(rows, n0 + per);
+    for (int64_t b = (int64_t)tid * 128; b < (int64_t)(n1 - n0) * ad.rank * 2; b += kUpThreads * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(ad.b + (int64_t)n0 * ad.rank) + b));
+    if (tid < kFewTokens) token[tid] = tile.token(min(tid, tile.count - 1));
+    __syncthreads();
+    const int steps = (cols + 31) / 32;
+    for (int m = 0; m < tile.count; m += 16) {
+        float acc[NT][4] = {};
+        const uint16_t* const x0 = x + (int64_t)token[min(m + g, kFewTokens - 1)] * ldx + 8 * q;
+        const uint16_t* const x1 = x + (int64_t)token[min(m + g + 8, kFewTokens - 1)] * ldx + 8 * q;
+#pragma unroll 2
+        for (int c = me * 8 + warp; c < steps; c += 8 * kFewParts) {
+            const bool in = 32 * c + 8 * q < cols;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            const uint4 z0 = in ? *reinterpret_cast<const uint4*>(x0 + 32 * c) : none;
+            const uint4 z1 = in ? *reinterpret_cast<const uint4*>(x1 + 32 * c) : none;
+            uint4 f[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int r = 8 * j + g;
+                f[j] = in && r < ad.rank ? *reinterpret_cast<const uint4*>(ad.a + (int64_t)r * cols + 32 * c + 8 * q) : none;
+            }
+            const uint32_t lo[4] = {z0.x, z1.x, z0.y, z1.y}, hi[4] = {z0.z, z1.z, z0.w, z1.w};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if (8 * j >= ad.rank) continue;
+                mma_bf16(acc[j], lo, f[j].x, f[j].y);
+                mma_bf16(acc[j], hi, f[j].z, f[j].w);
+            }
+        }
+        float* const mine = part + warp * 16 * SR;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            *reinterpret_cast<float2*>(mine + g * SR + 8 * j + 2 * q) = make_float2(acc[j][0], acc[j][1]);
+            *reinterpret_cast<float2*>(mine + (g + 8) * SR + 8 * j + 2 * q) = make_float2(acc[j][2], acc[j][3]);
+        }
+        __syncthreads();
+        for (int i = tid; i < 16 * wide / 4; i += kUpThreads) {
+            const int t = i / (wide / 4), r = i % (wide / 4) * 4;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>(part + (w * 16 + t) * SR + r);
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+            *reinterpret_cast<float4*>(all + (m + t) * SR + r) = s;
+        }
+        __syncthreads();
+    }
+    cluster_sync();
+    const uint32_t us = smem_addr(raw + FewShape<KS>::kAll);
+    for (int i = tid; i < tile.count * wide / 4; i += kUpThreads) {
+        const int t = i / (wide / 4), r = i % (wide / 4) * 4;
+        uint2 hi, lo;
+        split_bf16(sum_cluster(all + t * SR + r, kFewParts), &hi, &lo);
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + r) * 2), "r"(hi.x), "r"(hi.y) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + KS * 16 + r) * 2), "r"(lo.x), "r"(lo.y)
+                     : "memory");
+        if (t % kFewParts == me) {
+            uint16_t* const out = u + (int64_t)token[t] * 2 * wide_max + r;
+            *reinterpret_cast<uint2*>(out) = hi;
+            *reinterpret_cast<uint2*>(out + wide_max) = lo;
+        }
+    }
+    asm volatile("barrier.cluster.arrive;" ::: "memory");  // done with the others' shared memory
+    __syncthreads();
+    const uint32_t ys = us + (uint32_t)UpShape<KS>::u_bytes(kFewTokens) + warp * kUpAhead * 1024 + lane * 16;
+    for (int n = n0 + warp * 32; n < n1; n += 256)
+        up_columns<KS>(ad, 0, tile.count, token, us, ys, n, n1, y, ldy, [] {});
+    asm volatile("barrier.cluster.wait;" ::: "memory");    // and they with this CTA's
 }
 
 // ---------------------------------------------------------------- factors turned for the backward pass
