@@ -219,11 +219,17 @@ int64_t tiles_of(const qf_lora_batch& c, int n) {
     return c.d_plan ? qf::plan_tiles(c.tokens, n) : (c.tokens + kLoraTile - 1) / kLoraTile;
 }
 
+#ifndef QF_FEW_TOKENS
+#define QF_FEW_TOKENS 256       // at most so many tokens, and so many per adapter on average,
+#endif
+#ifndef QF_FEW_PER
+#define QF_FEW_PER 16           // take the one-launch kernel
+#endif
 template <int MAXA, int KS>
 qf_status few(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const qf_lora_batch& c, int wide,
               cudaStream_t s) {
     return launch(qf::k_lora_few<MAXA, KS>, dim3((unsigned)tiles * qf::kFewParts), qf::kUpThreads,
-                  qf::FewShape<KS>::kSmem, s, false, dim3(qf::kFewParts), A, P, static_cast<const uint16_t*>(c.x),
+                  qf::FewShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16)), s, false, dim3(qf::kFewParts), A, P, static_cast<const uint16_t*>(c.x),
                   c.ldx, (int)c.cols, static_cast<uint16_t*>(c.u), wide, (int)c.rows, static_cast<uint16_t*>(c.y),
                   c.ldy);
 }
@@ -234,7 +240,7 @@ qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int wide, cudaS
     fill(A, l, n);
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
-    if (c.tokens <= qf::kFewTokens) {
+    if (c.tokens <= QF_FEW_TOKENS && c.tokens <= QF_FEW_PER * (int64_t)n) {
         if (wide <= 16) return few<MAXA, 1>(A, P, tiles, c, wide, s);
         if (wide <= 32) return few<MAXA, 2>(A, P, tiles, c, wide, s);
         if (wide <= 64) return few<MAXA, 4>(A, P, tiles, c, wide, s);

@@ -181,10 +181,6 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void ldmatrix(uint32_t* r, uint32_t at) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
-}
 __device__ __forceinline__ uint32_t bf16x2(float hi, float lo) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -538,90 +534,113 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
 // stride ldy), read, added to in FP32 and rounded once.  Twice the bytes of the reductions
 // above for half the products: mma.sync keeps up here, and its accumulators lie in the
 // registers of the lanes that own y (tcgen05 with y tiles through shared memory and TMEM
-// took 95 us where this form takes 82).  A warp owns 32 columns of the tile's tokens and
+// took 95 us where this form takes 75).  A warp owns 32 columns of the tile's tokens and
 // keeps their factor rows as fragments; the columns are dealt to the four 8-wide MMA tiles
 // so that a lane ends up with 8 neighbouring columns of its rows: y moves in 16-byte
 // vectors, 64 bytes per row, four groups of 16 tokens ahead (cp.async, each lane exactly
 // what it will read itself, so without barriers).  u comes once per CTA.
-// KS: 16-deep rank steps.
+// Reduction index: steps of 32 positions of [high parts | low parts], permuted alike on both
+// operands so that 16 bytes of a row are a lane's fragments of two MMAs.  Rank 16: one
+// step, its high and low parts; above: both padded to multiples of 32, and a low step meets
+// the same factor fragments as its high step.
+// KS: the largest rank / 16.
 constexpr int kUpThreads = 256, kUpAhead = 4;
+__device__ __forceinline__ int up_pad(int rank) { return rank <= 16 ? 16 : (rank + 31) / 32 * 32; }
 template <int KS> struct UpShape {
-    static constexpr int kRow = 2 * KS * 16 + 8;          // u's row in shared memory, padded
+    static constexpr int kPad = KS == 1 ? 16 : (KS * 16 + 31) / 32 * 32;
+    static constexpr int kSteps = (kPad + 31) / 32;       // factor fragments
+    static constexpr int kRow = 2 * kPad + (kPad > 16 ? 32 : 0);   // u's row: an odd multiple of 64 bytes
     static constexpr size_t kRing = size_t(8) * kUpAhead * 2 * 512;
     __host__ __device__ static constexpr size_t u_bytes(int tokens) { return size_t(tokens) * kRow * 2; }
     __host__ __device__ static constexpr size_t smem(int tokens) { return u_bytes(tokens) + kRing; }
 };
-// A warp's 32 columns from n0 on.  us: u in shared memory ([tokens rounded up to 16][kRow]);
-// ys: this lane's part of the ring; ready(): called once, before u is read.
-template <int KS, typename READY>
-__device__ __forceinline__ void up_columns(const Adapter& ad, int backward, int count, const int* token, uint32_t us,
-                                           uint32_t ys, int n0, int width, uint16_t* y, int64_t ldy, READY ready) {
-    constexpr int UR = UpShape<KS>::kRow;
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, col = n0 + 8 * q, ks = (ad.rank + 15) / 16;
-    uint16_t* const ycol = y + col;
-    const bool inside = col < width;
-    auto fetch = [&](int m) {                              // 16 tokens: this lane's two rows
+// A warp's 32 columns from n0 on: the factor's fragments, and 16 tokens' y on the way.
+template <int KS>
+struct UpColumns {
+    uint4 f[UpShape<KS>::kSteps][4];
+    __device__ __forceinline__ void load_factor(const Adapter& ad, int backward, int n0, int width) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, pad = up_pad(ad.rank);
+        const uint16_t* const b = backward ? ad.a : ad.b;
+        const int ldf = backward ? (ad.rank + 15) / 16 * 16 : ad.rank;
+        const bool vec = (ldf & 7) == 0 && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
+        const bool even = (ldf & 1) == 0 && (reinterpret_cast<uintptr_t>(b) & 3) == 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = 16 * m + 8 * h + g;
-            if (inside && i < count)
-                cp_async16(ys + ((m % kUpAhead) * 2 + h) * 512, ycol + (int64_t)token[i] * ldy, true);
-        }
-        cp_async_commit();
-    };
+        for (int j = 0; j < 4; ++j) {
+            const int c = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
 #pragma unroll
-    for (int m = 0; m < kUpAhead; ++m) fetch(m);
-    uint32_t fv[KS][4][2];
-    const uint16_t* const f = backward ? ad.a : ad.b;
-    const int ldf = backward ? ks * 16 : ad.rank;
-    const bool vec = (ldf & 1) == 0 && (reinterpret_cast<uintptr_t>(f) & 3) == 0;
+            for (int k = 0; k < UpShape<KS>::kSteps; ++k) {
+                const int r = pad == 16 ? 8 * (q & 1) : 32 * k + 8 * q;
+                const uint16_t* const p = b + (int64_t)c * ldf + r;
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (c < width && r < ldf) {
+                    if (vec) {
+                        f[k][j] = *reinterpret_cast<const uint4*>(p);
+                        continue;
+                    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int c = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
-        const uint16_t* const p = f + (int64_t)c * ldf + 2 * q;
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 16 * k + 8 * h;
-                fv[k][j][h] = 0;
-                if (c >= width || r + 2 * q >= ldf) continue;
-                if (vec) fv[k][j][h] = *reinterpret_cast<const uint32_t*>(p + r);
-                else fv[k][j][h] = p[r] | (r + 2 * q + 1 < ldf ? (uint32_t)p[r + 1] << 16 : 0u);
+                    for (int i = 0; i < 4; ++i) {
+                        if (r + 2 * i >= ldf) continue;
+                        if (even) w[i] = *reinterpret_cast<const uint32_t*>(p + 2 * i);
+                        else w[i] = p[2 * i] | (r + 2 * i + 1 < ldf ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+                    }
+                }
+                f[k][j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-    }
-    ready();
-    const uint32_t ua = us + (((lane & 15) * UR) + (lane >> 4) * 8) * 2;
-    const int groups = (count + 15) / 16;
-    for (int m = 0; m < groups; ++m) {
-        float acc[4][4] = {};
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                if (k >= ks) break;
-                // rows behind the tile are stale shared memory: their products are not used
-                uint32_t a[4];
-                ldmatrix(a, ua + (16 * m * UR + p * KS * 16 + 16 * k) * 2);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma_bf16(acc[j], a, fv[k][j][0], fv[k][j][1]);
-            }
-        cp_async_wait<kUpAhead - 1>();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = 16 * m + 8 * h + g;
-            if (!inside || i >= count) continue;
-            const uint4 v = lds16(ys + ((m % kUpAhead) * 2 + h) * 512);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = bf16x2(__fmaf_rn(ad.scale, acc[j][2 * h + 1], __uint_as_float(w[j] & 0xFFFF0000u)),
-                              __fmaf_rn(ad.scale, acc[j][2 * h], __uint_as_float(w[j] << 16)));
-            *reinterpret_cast<uint4*>(ycol + (int64_t)token[i] * ldy) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        fetch(m + kUpAhead);
     }
-    cp_async_wait<0>();
+};
+template <int AHEAD>
+__device__ __forceinline__ void fetch_y(int m, int count, const int* token, uint32_t ys, int n0, int width,
+                                        const uint16_t* y, int64_t ldy) {
+    const int lane = threadIdx.x & 31, col = n0 + 8 * (lane & 3);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = 16 * m + 8 * h + (lane >> 2);
+        if (col < width && i < count)
+            cp_async16(ys + ((m % AHEAD) * 2 + h) * 512, y + (int64_t)token[i] * ldy + col, true);
+    }
+    cp_async_commit();
+}
+// Tokens 16m .. 16m + 15 of the tile against the columns' fragments; us: u in shared memory,
+// [tokens][kRow]: high parts, then (at pad) low parts.
+template <int KS>
+__device__ __forceinline__ void up_products(const UpColumns<KS>& C, int pad, int m, uint32_t us, float (*acc)[4]) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t at = us + ((16 * m + (lane >> 2)) * UpShape<KS>::kRow + 8 * (lane & 3)) * 2;
+#pragma unroll
+    for (int k = 0; k < UpShape<KS>::kSteps; ++k) {
+        if (32 * k >= pad) break;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            if (p == 1 && pad == 16) break;                // (its only step holds both parts)
+            // rows behind the tile are stale shared memory: their products are not used
+            const uint4 u0 = lds16(at + (p * pad + 32 * k) * 2);
+            const uint4 u1 = lds16(at + (8 * UpShape<KS>::kRow + p * pad + 32 * k) * 2);
+            const uint32_t lo[4] = {u0.x, u1.x, u0.y, u1.y}, hi[4] = {u0.z, u1.z, u0.w, u1.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mma_bf16(acc[j], lo, C.f[k][j].x, C.f[k][j].y);
+                mma_bf16(acc[j], hi, C.f[k][j].z, C.f[k][j].w);
+            }
+        }
+    }
+}
+template <int AHEAD>
+__device__ __forceinline__ void add_to_y(int m, int count, const int* token, uint32_t ys, int n0, int width, uint16_t* y,
+                                         int64_t ldy, float scale, const float (*acc)[4]) {
+    const int lane = threadIdx.x & 31, col = n0 + 8 * (lane & 3);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = 16 * m + 8 * h + (lane >> 2);
+        if (col >= width || i >= count) continue;
+        const uint4 v = lds16(ys + ((m % AHEAD) * 2 + h) * 512);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = bf16x2(__fmaf_rn(scale, acc[j][2 * h + 1], __uint_as_float(w[j] & 0xFFFF0000u)),
+                          __fmaf_rn(scale, acc[j][2 * h], __uint_as_float(w[j] << 16)));
+        *reinterpret_cast<uint4*>(y + (int64_t)token[i] * ldy + col) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 template <int MAXA, int KS>
@@ -637,41 +656,52 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
     const Tile tile = tile_of(P, blockIdx.x / across);
     if (tile.count <= 0) return;
     const Adapter ad = A.t[tile.adapter];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ks = (ad.rank + 15) / 16, rows = min(kLoraTile, (P.tokens + 15) / 16 * 16);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n0 = (int)(blockIdx.x % across) * 256 + warp * 32;
+    const int wide = (ad.rank + 15) / 16 * 16, pad = up_pad(ad.rank), rows = min(kLoraTile, (P.tokens + 15) / 16 * 16);
     const uint32_t us = smem_addr(raw);
     const uint32_t ys = us + (uint32_t)UpShape<KS>::u_bytes(rows) + warp * kUpAhead * 1024 + lane * 16;
     if (tid < kLoraTile) token[tid] = tile.token(min(tid, tile.count - 1));
     __syncthreads();
-    for (int i = tid; i < tile.count * ks * 4; i += kUpThreads) {
-        const int t = i / (ks * 4), c = i % (ks * 4) * 8;          // high parts, then low parts
-        const bool low = c >= ks * 16;
-        cp_async16(us + (t * UR + (low ? KS * 16 + c - ks * 16 : c)) * 2,
-                   u + (int64_t)token[t] * 2 * wide_max + (low ? wide_max + c - ks * 16 : c), true);
+    for (int i = tid; i < tile.count * (pad / 4); i += kUpThreads) {
+        const int t = i / (pad / 4), c = i % (pad / 4) * 8, r = c < pad ? c : c - pad;   // high parts, low parts
+        cp_async16(us + (t * UR + c) * 2, u + (int64_t)token[t] * 2 * wide_max + (r < wide ? (c < pad ? r : wide_max + r) : 0),
+                   r < wide);
     }
     cp_async_commit();
-    up_columns<KS>(ad, backward, tile.count, token, us, ys, (int)(blockIdx.x % across) * 256 + warp * 32, width, y, ldy,
-                   [] {
-                       cp_async_wait<kUpAhead>();
-                       __syncthreads();                    // u is there for every warp
-                   });
+#pragma unroll
+    for (int m = 0; m < kUpAhead; ++m) fetch_y<kUpAhead>(m, tile.count, token, ys, n0, width, y, ldy);
+    UpColumns<KS> C;
+    C.load_factor(ad, backward, n0, width);
+    cp_async_wait<kUpAhead>();
+    __syncthreads();                                       // u is there for every warp
+    const int groups = (tile.count + 15) / 16;
+    for (int m = 0; m < groups; ++m) {
+        float acc[4][4] = {};
+        up_products<KS>(C, pad, m, us, acc);
+        cp_async_wait<kUpAhead - 1>();
+        add_to_y<kUpAhead>(m, tile.count, token, ys, n0, width, y, ldy, ad.scale, acc);
+        fetch_y<kUpAhead>(m + kUpAhead, tile.count, token, ys, n0, width, y, ldy);
+    }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- few tokens: down and up in one launch
 //
 // Decoding batches: a handful of tokens per adapter, so the factors are most of the bytes
 // and launches and waits most of the time.  A cluster of eight CTAs takes one tile: each
-// forms its eighth of the depth (mma.sync straight from registers: the 16 bytes a lane
-// loads are its fragments, with the reduction index permuted alike on both operands), all
+// forms its eighth of the depth (mma.sync straight from registers, permuted as above), all
 // of them add the eight parts through distributed shared memory, each then does its eighth
-// of the columns.  The slice of B is on its way to L2 meanwhile.
-constexpr int kFewParts = 8, kFewTokens = 64;
+// of the columns, the factor and y of the next 32 columns always on the way; those of the
+// first before the sums are waited for, the rest of B's slice to L2 at the very start.
+constexpr int kFewParts = 8, kFewAhead = 2;
 template <int KS> struct FewShape {
     static constexpr int kSum = KS * 16 + 4;              // floats per token of a partial u
-    static constexpr size_t kPart = size_t(8) * 16 * kSum * 4;      // a warp's 16 tokens each
-    static constexpr size_t kAll = size_t(kFewTokens) * kSum * 4;   // the CTA's
-    static constexpr size_t kWork = kPart > UpShape<KS>::smem(kFewTokens) ? kPart : UpShape<KS>::smem(kFewTokens);
-    static constexpr size_t kSmem = kAll + kWork;
+    static constexpr size_t kPart = size_t(8) * 16 * kSum * 4;                // the warps' 16 tokens each
+    static size_t all(int rows) { return size_t(rows) * kSum * 4; }           // the CTA's tokens
+    static size_t smem(int rows) {
+        return all(rows) + (kPart > UpShape<KS>::u_bytes(rows) ? kPart : UpShape<KS>::u_bytes(rows)) +
+               size_t(2) * 8 * kFewAhead * 1024;
+    }
 };
 template <int MAXA, int KS>
 __global__ void __launch_bounds__(kUpThreads)
@@ -679,26 +709,32 @@ k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const
            int cols, uint16_t* __restrict__ u, int wide_max, int rows, uint16_t* y, int64_t ldy) {
     constexpr int SR = FewShape<KS>::kSum, UR = UpShape<KS>::kRow, NT = KS * 2;
     extern __shared__ __align__(16) unsigned char raw[];
-    __shared__ int token[kFewTokens];
-    float* const all = reinterpret_cast<float*>(raw);
-    float* const part = reinterpret_cast<float*>(raw + FewShape<KS>::kAll);
+    __shared__ int token[kLoraTile];
     const Tile tile = tile_of(P, blockIdx.x / kFewParts);
     if (tile.count <= 0) return;                          // the same for the whole cluster
     const Adapter ad = A.t[tile.adapter];
     const int me = blockIdx.x % kFewParts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, q = lane & 3, wide = (ad.rank + 15) / 16 * 16;
+    const int g = lane >> 2, q = lane & 3, wide = (ad.rank + 15) / 16 * 16, pad = up_pad(ad.rank);
+    const int room = min(kLoraTile, (P.tokens + 15) / 16 * 16);
+    unsigned char* at = raw;
+    const uint32_t ys = smem_addr(at) + warp * 2 * kFewAhead * 1024 + lane * 16;
+    at += 2 * 8 * kFewAhead * 1024;
+    float* const all = reinterpret_cast<float*>(at);
+    at += (size_t)room * SR * 4;
+    float* const part = reinterpret_cast<float*>(at);     // then u
+    const uint32_t us = smem_addr(at);
     // this CTA's columns of y: whole 32-column groups, shared out evenly
     const int per = ((rows + 31) / 32 + kFewParts - 1) / kFewParts * 32, n0 = me * per, n1 = min(rows, n0 + per);
     for (int64_t b = (int64_t)tid * 128; b < (int64_t)(n1 - n0) * ad.rank * 2; b += kUpThreads * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(ad.b + (int64_t)n0 * ad.rank) + b));
-    if (tid < kFewTokens) token[tid] = tile.token(min(tid, tile.count - 1));
+    if (tid < kLoraTile) token[tid] = tile.token(min(tid, tile.count - 1));
     __syncthreads();
     const int steps = (cols + 31) / 32;
     for (int m = 0; m < tile.count; m += 16) {
         float acc[NT][4] = {};
-        const uint16_t* const x0 = x + (int64_t)token[min(m + g, kFewTokens - 1)] * ldx + 8 * q;
-        const uint16_t* const x1 = x + (int64_t)token[min(m + g + 8, kFewTokens - 1)] * ldx + 8 * q;
-#pragma unroll 2
+        const uint16_t* const x0 = x + (int64_t)token[m + g] * ldx + 8 * q;
+        const uint16_t* const x1 = x + (int64_t)token[m + g + 8] * ldx + 8 * q;
+#pragma unroll (KS == 1 ? 4 : 2)
         for (int c = me * 8 + warp; c < steps; c += 8 * kFewParts) {
             const bool in = 32 * c + 8 * q < cols;
             const uint4 none = make_uint4(0, 0, 0, 0);
@@ -740,16 +776,24 @@ k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const
         }
         __syncthreads();
     }
+    const int groups = (tile.count + 15) / 16;
+    const auto column = [&](int i) { return n0 + (warp + 8 * i) * 32; };
+    const auto ring = [&](int i) { return ys + (i & 1) * kFewAhead * 1024; };
+    const auto fetch = [&](int i) {
+        for (int m = 0; m < kFewAhead; ++m) fetch_y<kFewAhead>(m, tile.count, token, ring(i), column(i), n1, y, ldy);
+    };
+    UpColumns<KS> C;
+    C.load_factor(ad, 0, column(0), n1);
+    fetch(0);
     cluster_sync();
-    const uint32_t us = smem_addr(raw + FewShape<KS>::kAll);
-    for (int i = tid; i < tile.count * wide / 4; i += kUpThreads) {
-        const int t = i / (wide / 4), r = i % (wide / 4) * 4;
-        uint2 hi, lo;
-        split_bf16(sum_cluster(all + t * SR + r, kFewParts), &hi, &lo);
+    for (int i = tid; i < tile.count * pad / 4; i += kUpThreads) {
+        const int t = i / (pad / 4), r = i % (pad / 4) * 4;
+        uint2 hi = make_uint2(0, 0), lo = make_uint2(0, 0);
+        if (r < wide) split_bf16(sum_cluster(all + t * SR + r, kFewParts), &hi, &lo);
         asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + r) * 2), "r"(hi.x), "r"(hi.y) : "memory");
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + KS * 16 + r) * 2), "r"(lo.x), "r"(lo.y)
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + pad + r) * 2), "r"(lo.x), "r"(lo.y)
                      : "memory");
-        if (t % kFewParts == me) {
+        if (t % kFewParts == me && r < wide) {
             uint16_t* const out = u + (int64_t)token[t] * 2 * wide_max + r;
             *reinterpret_cast<uint2*>(out) = hi;
             *reinterpret_cast<uint2*>(out + wide_max) = lo;
@@ -757,9 +801,27 @@ k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const
     }
     asm volatile("barrier.cluster.arrive;" ::: "memory");  // done with the others' shared memory
     __syncthreads();
-    const uint32_t ys = us + (uint32_t)UpShape<KS>::u_bytes(kFewTokens) + warp * kUpAhead * 1024 + lane * 16;
-    for (int n = n0 + warp * 32; n < n1; n += 256)
-        up_columns<KS>(ad, 0, tile.count, token, us, ys, n, n1, y, ldy, [] {});
+    for (int i = 0; column(i) < n1; ++i) {
+        UpColumns<KS> next;
+        const bool more = column(i + 1) < n1;
+        if (more) next.load_factor(ad, 0, column(i + 1), n1);
+        if (groups <= kFewAhead) {                          // the next columns' y fits beside these
+            fetch(i + 1);
+            cp_async_wait<kFewAhead>();
+        } else {
+            cp_async_wait<0>();
+        }
+        for (int m = 0; m < groups; ++m) {
+            float acc[4][4] = {};
+            up_products<KS>(C, pad, m, us, acc);
+            if (groups > kFewAhead && m > 0) cp_async_wait<kFewAhead - 1>();
+            add_to_y<kFewAhead>(m, tile.count, token, ring(i), column(i), n1, y, ldy, ad.scale, acc);
+            if (groups > kFewAhead) fetch_y<kFewAhead>(m + kFewAhead, tile.count, token, ring(i), column(i), n1, y, ldy);
+        }
+        if (groups > kFewAhead && more) fetch(i + 1);
+        if (more) C = next;
+    }
+    cp_async_wait<0>();
     asm volatile("barrier.cluster.wait;" ::: "memory");    // and they with this CTA's
 }
 
