@@ -60,7 +60,7 @@ qf_status check_batch(const qf_lora* l, int n, const qf_lora_batch& c, int* max_
                     (long long)c.rows, (long long)c.cols);
     if (c.d_plan == nullptr && n != 1)
         return fail(QF_ERR_INVALID_ARG, "without a plan there is one adapter, not %d", n);
-    if ((reinterpret_cast<uintptr_t>(c.d_plan) & 3) != 0) return fail(QF_ERR_ALIGN, "plan not 4-byte aligned");
+    if (!aligned16(c.d_plan)) return fail(QF_ERR_ALIGN, "plan not 16-byte aligned");
     *max_rank = 0;
     for (int i = 0; i < n; ++i) {
         if (l[i].rank < 1 || l[i].rank > kLoraMaxRank)
@@ -80,11 +80,11 @@ qf_status check_u(const qf_lora_batch& c) {
     return QF_OK;
 }
 
-// One launch, optionally as a programmatic dependent of the kernel before it (each kernel
-// here waits for that one's results first) and in clusters.
+// One launch as a programmatic dependent of the kernel before it, in clusters.  Every kernel
+// here waits for that one's end before it touches memory that may depend on it, and before
+// it lets the next one start.
 template <typename K, typename... Args>
-qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, bool dependent,
-                 dim3 cluster, Args... args) {
+qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, dim3 cluster, Args... args) {
     Shape shape;                                   // (also raises the shared-memory limit once)
     const qf_status st = shape_of(kernel, threads, smem, &shape);
     if (st != QF_OK) return st;
@@ -95,10 +95,8 @@ qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, 
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int k = 0;
-    if (dependent) {
-        attr[k].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[k++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    attr[k].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[k++].val.programmaticStreamSerializationAllowed = 1;
     if (cluster.x * cluster.y * cluster.z > 1) {
         attr[k].id = cudaLaunchAttributeClusterDimension;
         attr[k].val.clusterDim.x = cluster.x;
@@ -153,7 +151,7 @@ int parts_for(int64_t units, int64_t steps, int64_t slots) {
 
 template <int MAXA>
 qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
-               int64_t depth, bool backward, void* u, int wide, bool dependent, cudaStream_t s) {
+               int64_t depth, bool backward, void* u, int wide, cudaStream_t s) {
     qf::RowMaps map{};
     if (depth > 0) {
         const qf_status st = row_maps(&map, z, P.tokens, depth, ldz);
@@ -162,7 +160,7 @@ qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, co
     const int parts = parts_for(tiles, (depth + 255) / 256, 148 * QF_DOWN_SLOTS);
     if (tiles * parts > INT32_MAX) return fail(QF_ERR_SHAPE, "too many tokens for one launch");
     return launch(qf::k_lora_down<MAXA>, dim3((unsigned)(tiles * parts)), qf::kTcThreads, qf::down_smem(wide), s,
-                  dependent, dim3(parts), A, P, map, (int)depth, (int)backward, parts, static_cast<uint16_t*>(u),
+                  dim3(parts), A, P, map, (int)depth, (int)backward, parts, static_cast<uint16_t*>(u),
                   wide);
 }
 
@@ -172,7 +170,7 @@ qf_status up_ks(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, c
     const int64_t blocks = tiles * ((width + 255) / 256);
     if (blocks > INT32_MAX) return fail(QF_ERR_SHAPE, "tokens x width too large for one launch");
     return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), qf::kUpThreads,
-                  qf::UpShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16)), s, true,
+                  qf::UpShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16)), s,
                   dim3(1), A, P, static_cast<const uint16_t*>(u), wide, (int)width, (int)backward,
                   static_cast<uint16_t*>(y), ldy);
 }
@@ -187,7 +185,7 @@ qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, cons
 
 template <int MAXA>
 qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf_lora_batch& c, const void* v,
-                const void* gy, int64_t ldgy, int wide, cudaStream_t s) {
+                const void* gy, int64_t ldgy, int wide, bool beside, cudaStream_t s) {
     qf::RowMaps x{}, y{}, vm{}, um{};
     qf_status st = QF_OK;
     if (c.tokens > 0) {
@@ -201,8 +199,8 @@ qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf
     int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens, 148 * QF_GRAD_SLOTS);
     while (parts & (parts - 1)) --parts;          // its CTAs share a tile's 128 columns evenly
     return launch(qf::k_lora_grad<MAXA>, dim3((unsigned)tiles, n, parts), qf::kTcThreads,
-                  qf::grad_smem(wide), s, true, dim3(1, 1, parts), G, P, x, (int)c.cols, vm, y, (int)c.rows, um,
-                  wide);
+                  qf::grad_smem(wide), s, dim3(1, 1, parts), G, P, x, (int)c.cols, vm, y, (int)c.rows, um,
+                  wide, (int)beside);
 }
 
 template <int MAXA>
@@ -229,7 +227,7 @@ template <int MAXA, int KS>
 qf_status few(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const qf_lora_batch& c, int wide,
               cudaStream_t s) {
     return launch(qf::k_lora_few<MAXA, KS>, dim3((unsigned)tiles * qf::kFewParts), qf::kUpThreads,
-                  qf::FewShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16)), s, false, dim3(qf::kFewParts), A, P, static_cast<const uint16_t*>(c.x),
+                  qf::FewShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16)), s, dim3(qf::kFewParts), A, P, static_cast<const uint16_t*>(c.x),
                   c.ldx, (int)c.cols, static_cast<uint16_t*>(c.u), wide, (int)c.rows, static_cast<uint16_t*>(c.y),
                   c.ldy);
 }
@@ -246,7 +244,7 @@ qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int wide, cudaS
         if (wide <= 64) return few<MAXA, 4>(A, P, tiles, c, wide, s);
         return few<MAXA, 8>(A, P, tiles, c, wide, s);
     }
-    qf_status st = down<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, wide, false, s);
+    qf_status st = down<MAXA>(A, P, tiles, c.x, c.ldx, c.cols, false, c.u, wide, s);
     if (st != QF_OK || c.rows == 0) return st;
     return up<MAXA>(A, P, tiles, c.u, wide, c.rows, false, c.y, c.ldy, s);
 }
@@ -271,7 +269,7 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
     }
     const int64_t work = (c.cols + c.rows) * (wide / 8);
     const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((work + 255) / 256, 1024));
-    qf_status st = launch(qf::k_lora_turn<MAXA>, dim3((unsigned)blocks, n), 256, 0, s, false, dim3(1), T,
+    qf_status st = launch(qf::k_lora_turn<MAXA>, dim3((unsigned)blocks, n), 256, 0, s, dim3(1), T,
                           (int)c.rows, (int)c.cols);
     if (st != QF_OK) return st;
     for (int i = 0; i < n; ++i) {
@@ -281,7 +279,7 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
     if (c.tokens > 0) {
-        st = down<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, wide, true, s);
+        st = down<MAXA>(A, P, tiles, gy, ldgy, c.rows, true, v, wide, s);
         if (st != QF_OK) return st;
         if (gx && c.cols > 0) {
             st = up<MAXA>(A, P, tiles, v, wide, c.cols, true, gx, ldgx, s);
@@ -295,7 +293,7 @@ qf_status backward(const qf_lora* l, const qf_lora_grad* g, int n, const qf_lora
         G.scale[i] = l[i].scale;
         G.rank[i] = l[i].rank;
     }
-    return grads<MAXA>(G, P, n, c, v, gy, ldgy, wide, s);
+    return grads<MAXA>(G, P, n, c, v, gy, ldgy, wide, gx && c.tokens > 0 && c.cols > 0, s);
 }
 
 }  // namespace
@@ -318,14 +316,12 @@ qf_status qf_lora_plan(const int32_t* d_index, int64_t tokens, int n_adapters, v
     if (d_plan == nullptr || plan_bytes < qf_lora_plan_bytes(tokens, n_adapters))
         return fail(QF_ERR_INVALID_ARG, "plan of %zu bytes, %zu needed", d_plan ? plan_bytes : (size_t)0,
                     qf_lora_plan_bytes(tokens, n_adapters));
-    if (((reinterpret_cast<uintptr_t>(d_index) | reinterpret_cast<uintptr_t>(d_plan)) & 3) != 0)
-        return fail(QF_ERR_ALIGN, "d_index or d_plan not 4-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(d_index) & 3) != 0 || !aligned16(d_plan))
+        return fail(QF_ERR_ALIGN, "d_index not 4-byte or d_plan not 16-byte aligned");
     if (overlap(d_index, 4 * tokens, d_plan, (int64_t)plan_bytes))
         return fail(QF_ERR_INVALID_ARG, "d_index and d_plan overlap");
-    qf::k_lora_plan<<<n_adapters, qf::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        d_index, (int)tokens, n_adapters, static_cast<int32_t*>(d_plan));
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? QF_OK : cuda_fail(e, "kernel launch");
+    return launch(qf::k_lora_plan, dim3(n_adapters), qf::kPlanThreads, 0, static_cast<cudaStream_t>(stream), dim3(1),
+                  d_index, (int)tokens, n_adapters, static_cast<int32_t*>(d_plan));
 }
 
 qf_status qf_lora_apply(const qf_lora* l, int n, const qf_lora_batch* batch, void* stream) {

@@ -31,8 +31,8 @@ struct AdapterTable {
     Adapter t[MAXA];
 };
 
-// Device plan, int32 words: head | start[n + 1] | order[tokens] | per tile: adapter (-1:
-// empty), begin
+// Device plan, int32 words: head | per tile: adapter, begin, count (0: empty), 0 |
+// start[n + 1] | order[tokens].  A tile's record is one load beside the head's.
 struct PlanView {
     const int32_t* w;                   // NULL: every token has adapter 0, in order
     int tokens;
@@ -42,7 +42,7 @@ __host__ __device__ inline int64_t plan_tiles(int64_t tokens, int64_t n) {
     return (tokens + kLoraTile - 1) / kLoraTile + (n < tokens ? n : tokens);
 }
 __host__ __device__ inline int64_t plan_words(int64_t tokens, int64_t n) {
-    return kPlanHead + n + 1 + tokens + 2 * plan_tiles(tokens, n);
+    return kPlanHead + 4 * plan_tiles(tokens, n) + n + 1 + tokens;
 }
 
 #ifdef __CUDACC__
@@ -59,8 +59,10 @@ __device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcon
 // leaves room for each run's short last tile without knowing the other runs' lengths;
 // slots left over are empty tiles.  Latency-bound: every CTA reads the index from L2.
 __global__ void __launch_bounds__(kPlanThreads)
-k_lora_plan(const int32_t* __restrict__ index, int tokens, int n, int32_t* __restrict__ plan) {
+k_lora_plan(const int32_t* index, int tokens, int n, int32_t* __restrict__ plan) {
     constexpr int kWarps = kPlanThreads / 32, kAhead = 8;
+    wait_previous_grid();
+    let_next_grid_start();
     __shared__ unsigned char occurs[kLoraMaxAdapters];
     __shared__ int warp_own[kWarps], warp_less[kWarps], warp_seen[kWarps];
     const int a = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -92,18 +94,16 @@ k_lora_plan(const int32_t* __restrict__ index, int tokens, int n, int32_t* __res
         warp_seen[warp] = seen;
     }
     __syncthreads();
-    int start = 0, count = 0, before = 0, first = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) before = count;
-        count += warp_own[w];
-        start += warp_less[w];
-        first += warp_seen[w];
-    }
+    static_assert(kWarps == 32, "one lane per warp below");
+    const int o = warp_own[lane], count = __reduce_add_sync(0xFFFFFFFFu, o);
+    const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? o : 0);
+    const int start = __reduce_add_sync(0xFFFFFFFFu, warp_less[lane]);
+    int first = __reduce_add_sync(0xFFFFFFFFu, warp_seen[lane]);
     first += start / kLoraTile;
     const int behind = count > 0 ? (start + count) / kLoraTile - start / kLoraTile + 1 : 0;
-    int32_t* const starts = plan + kPlanHead;
+    int4* const tiles = reinterpret_cast<int4*>(plan + kPlanHead);
+    int32_t* const starts = plan + kPlanHead + 4 * plan_tiles(tokens, n);
     int32_t* const order = starts + n + 1;
-    int32_t* const tiles = order + tokens;
     if (tid == 0) {
         starts[a] = start;
         if (a == n - 1) {
@@ -114,10 +114,8 @@ k_lora_plan(const int32_t* __restrict__ index, int tokens, int n, int32_t* __res
             plan[3] = n;
         }
     }
-    for (int i = tid; i < behind; i += kPlanThreads) {
-        tiles[2 * (first + i)] = i * kLoraTile < count ? a : -1;
-        tiles[2 * (first + i) + 1] = start + i * kLoraTile;
-    }
+    for (int i = tid; i < behind; i += kPlanThreads)
+        tiles[first + i] = make_int4(a, start + i * kLoraTile, max(0, min(kLoraTile, count - i * kLoraTile)), 0);
     if (own == 0) return;
     int32_t* out = order + start + before;
     for (int t = t0; t < t1; t += 32 * kAhead) {
@@ -148,14 +146,13 @@ __device__ __forceinline__ Tile tile_of(const PlanView& P, int i) {
         t.count = max(0, min(kLoraTile, P.tokens - t.begin));
         return t;
     }
-    if (P.w[2] != P.tokens || P.w[3] != P.n || i >= P.w[0]) return t;   // not this batch's plan
-    const int32_t* const start = P.w + kPlanHead;
-    t.order = start + P.n + 1;
-    const int a = t.order[P.tokens + 2 * i];
-    if (a < 0) return t;
-    t.adapter = a;
-    t.begin = t.order[P.tokens + 2 * i + 1];
-    t.count = min(kLoraTile, start[a + 1] - t.begin);
+    const int4 head = *reinterpret_cast<const int4*>(P.w);
+    const int4 tile = *reinterpret_cast<const int4*>(P.w + kPlanHead + 4 * (int64_t)i);
+    if (head.z != P.tokens || head.w != P.n || i >= head.x) return t;   // not this batch's plan, or no such tile
+    t.order = P.w + kPlanHead + 4 * plan_tiles(P.tokens, P.n) + P.n + 1;
+    t.adapter = tile.x;
+    t.begin = tile.y;
+    t.count = tile.z;
     return t;
 }
 __device__ __forceinline__ Tile run_of(const PlanView& P, int adapter) {   // an adapter's whole run
@@ -164,11 +161,12 @@ __device__ __forceinline__ Tile run_of(const PlanView& P, int adapter) {   // an
         t.count = P.tokens;
         return t;
     }
-    if (P.w[2] != P.tokens || P.w[3] != P.n) {
+    const int4 head = *reinterpret_cast<const int4*>(P.w);
+    if (head.z != P.tokens || head.w != P.n) {
         t.count = -1;
         return t;
     }
-    const int32_t* const start = P.w + kPlanHead;
+    const int32_t* const start = P.w + kPlanHead + 4 * plan_tiles(P.tokens, P.n);
     t.order = start + P.n + 1;
     t.begin = start[adapter];
     t.count = start[adapter + 1] - t.begin;
@@ -650,11 +648,14 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
     constexpr int UR = UpShape<KS>::kRow;
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ int token[kLoraTile];
-    wait_previous_grid();
-    let_next_grid_start();
+    // everything but u was there before the kernel that forms u let this one start
     const int across = (width + 255) / 256;
     const Tile tile = tile_of(P, blockIdx.x / across);
-    if (tile.count <= 0) return;
+    if (tile.count <= 0) {
+        wait_previous_grid();
+        let_next_grid_start();
+        return;
+    }
     const Adapter ad = A.t[tile.adapter];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n0 = (int)(blockIdx.x % across) * 256 + warp * 32;
     const int wide = (ad.rank + 15) / 16 * 16, pad = up_pad(ad.rank), rows = min(kLoraTile, (P.tokens + 15) / 16 * 16);
@@ -662,17 +663,19 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
     const uint32_t ys = us + (uint32_t)UpShape<KS>::u_bytes(rows) + warp * kUpAhead * 1024 + lane * 16;
     if (tid < kLoraTile) token[tid] = tile.token(min(tid, tile.count - 1));
     __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kUpAhead; ++m) fetch_y<kUpAhead>(m, tile.count, token, ys, n0, width, y, ldy);
+    UpColumns<KS> C;
+    C.load_factor(ad, backward, n0, width);
+    wait_previous_grid();
+    let_next_grid_start();
     for (int i = tid; i < tile.count * (pad / 4); i += kUpThreads) {
         const int t = i / (pad / 4), c = i % (pad / 4) * 8, r = c < pad ? c : c - pad;   // high parts, low parts
         cp_async16(us + (t * UR + c) * 2, u + (int64_t)token[t] * 2 * wide_max + (r < wide ? (c < pad ? r : wide_max + r) : 0),
                    r < wide);
     }
     cp_async_commit();
-#pragma unroll
-    for (int m = 0; m < kUpAhead; ++m) fetch_y<kUpAhead>(m, tile.count, token, ys, n0, width, y, ldy);
-    UpColumns<KS> C;
-    C.load_factor(ad, backward, n0, width);
-    cp_async_wait<kUpAhead>();
+    cp_async_wait<0>();
     __syncthreads();                                       // u is there for every warp
     const int groups = (tile.count + 15) / 16;
     for (int m = 0; m < groups; ++m) {
@@ -710,6 +713,8 @@ k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const
     constexpr int SR = FewShape<KS>::kSum, UR = UpShape<KS>::kRow, NT = KS * 2;
     extern __shared__ __align__(16) unsigned char raw[];
     __shared__ int token[kLoraTile];
+    wait_previous_grid();
+    let_next_grid_start();
     const Tile tile = tile_of(P, blockIdx.x / kFewParts);
     if (tile.count <= 0) return;                          // the same for the whole cluster
     const Adapter ad = A.t[tile.adapter];
@@ -837,6 +842,7 @@ struct TurnTable {
 template <int MAXA>
 __global__ void __launch_bounds__(256)
 k_lora_turn(const __grid_constant__ TurnTable<MAXA> A, int rows, int cols) {
+    wait_previous_grid();
     let_next_grid_start();
     const Adapter ad = A.t[blockIdx.y];
     const int wide = (ad.rank + 15) / 16 * 16;
@@ -893,16 +899,22 @@ template <int MAXA>
 __global__ void __launch_bounds__(kTcThreads)
 k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const __grid_constant__ RowMaps xmap,
             int cols, const __grid_constant__ RowMaps vmap, const __grid_constant__ RowMaps gymap, int rows,
-            const __grid_constant__ RowMaps umap, int wide_max) {
+            const __grid_constant__ RowMaps umap, int wide_max, int beside) {
     constexpr int RS = kGradCols + 4;
     extern __shared__ unsigned char raw[];
     __shared__ TcPipe<QF_GRAD_STAGES> pipe;
-    wait_previous_grid();
+    // beside: the kernel before this one is k_lora_up, which let this one start after it had
+    // waited for v; it needs nothing of that kernel and runs beside it, waiting for its end at
+    // its own (so that what follows this kernel follows both)
+    if (!beside) wait_previous_grid();
     let_next_grid_start();
     const int parts = gridDim.z, part = blockIdx.z, adapter = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Tile run = run_of(P, adapter);
-    if (run.count < 0) return;                            // not this batch's plan
+    if (run.count < 0) {                                  // not this batch's plan
+        if (beside) wait_previous_grid();
+        return;
+    }
     const int xt = (cols + kGradCols - 1) / kGradCols;
     const bool of_a = (int)blockIdx.x < xt;
     const int depth = of_a ? cols : rows, c0 = (of_a ? (int)blockIdx.x : (int)blockIdx.x - xt) * kGradCols;
@@ -1004,6 +1016,7 @@ k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const _
         }
     }
     if (parts > 1) cluster_sync();
+    if (beside) wait_previous_grid();
 }
 
 #endif  // __CUDACC__

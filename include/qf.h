@@ -521,7 +521,7 @@ size_t qf_grad_norm_workspace_bytes(void);
  *   d_index   DEVICE int32[tokens]: each token's adapter in [0, n_adapters); any other value
  *             (e.g. -1): none.  In any order: a request's tokens need not be neighbours.
  *   tokens    0 .. 2^26;  n_adapters  1 .. QF_LORA_MAX_ADAPTERS
- *   d_plan    DEVICE memory of qf_lora_plan_bytes(tokens, n_adapters) bytes, 4-byte aligned,
+ *   d_plan    DEVICE memory of qf_lora_plan_bytes(tokens, n_adapters) bytes, 16-byte aligned,
  *             overwritten.
  */
 qf_status qf_lora_plan(const int32_t* d_index, int64_t tokens, int n_adapters, void* d_plan,

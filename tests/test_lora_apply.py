@@ -94,12 +94,13 @@ def test_columns_of_one_buffer_do_not_overlap():
 def test_plan_refusals_and_sizes():
     call, size = qf.lib.qf_lora_plan, qf.lib.qf_lora_plan_bytes
     need = size(100, 3)
-    assert need == 4 * (4 + 4 + 100 + 2 * (1 + 3))
+    assert need == 4 * (4 + 4 * (1 + 3) + 4 + 100)
     assert size(-1, 3) == 0 and size(100, 0) == 0 and size(100, 513) == 0 and size((1 << 26) + 1, 1) == 0
     assert call(0x1000, 100, 0, 0x9000, need, None) == 1 and call(0x1000, 100, 513, 0x9000, need, None) == 1
     assert call(0x1000, -1, 3, 0x9000, need, None) == 2 and call(None, 100, 3, 0x9000, need, None) == 1
     assert call(0x1000, 100, 3, None, need, None) == 1 and call(0x1000, 100, 3, 0x9000, need - 1, None) == 1
-    assert call(0x1002, 100, 3, 0x9000, need, None) == 3 and call(0x1000, 100, 3, 0x1010, need, None) == 1
+    assert call(0x1002, 100, 3, 0x9000, need, None) == 3 and call(0x1000, 100, 3, 0x9004, need, None) == 3
+    assert call(0x1000, 100, 3, 0x1010, need, None) == 1
 
 
 def test_struct_layouts_match_the_header():
@@ -362,12 +363,13 @@ def test_plan_is_the_stable_sort(t, n):
     live = [(idx == i).nonzero().view(-1) for i in range(n)]
     counts = torch.tensor([len(x) for x in live])
     assert plan[1] == counts.sum()
-    assert torch.equal(plan[4:5 + n].long(), torch.cat([torch.zeros(1, dtype=torch.long), counts.cumsum(0)]))
-    assert torch.equal(plan[5 + n:5 + n + int(counts.sum())].long(), torch.cat(live))
-    tiles = plan[5 + n + t:].view(-1, 2)[:plan[0]].tolist()                # adapter or -1, begin
+    tiles, rest = plan[4:].split([4 * ((t + 127) // 128 + min(n, t)), n + 1 + t])
     start = [0] + counts.cumsum(0).tolist()
-    assert [x for x in tiles if x[0] >= 0] == [[i, start[i] + k] for i in range(n)
-                                               for k in range(0, int(counts[i]), 128)]
+    assert rest[:n + 1].tolist() == start
+    assert torch.equal(rest[n + 1:n + 1 + int(counts.sum())].long(), torch.cat(live))
+    tiles = tiles.view(-1, 4)[:plan[0]].tolist()                            # adapter, begin, count, 0
+    assert [x for x in tiles if x[2] > 0] == [[i, start[i] + k, min(128, int(counts[i]) - k), 0] for i in range(n)
+                                              for k in range(0, int(counts[i]), 128)]
 
 
 @pytest.mark.gpu
@@ -468,3 +470,31 @@ def test_offsets_past_32_bits():
     qf.qf_lora_apply(x, c.dad, y, c.u[:t], plan=c.plan)
     c.dev["y"].copy_(y)
     c.check_forward()
+
+
+@pytest.mark.gpu
+def test_captured_behind_copies_and_fills():
+    """The first kernel of each call behind a captured memcpy and memset."""
+    c = Batch(spread(300, 3, seed=16), 256, 264, [16, 8, 20], seed=16)
+    index, src = c.index.to(DEV), torch.empty_like(c.index.to(DEV))
+    src.copy_(index)
+    y0, gx0 = c.dev["y"].clone(), c.dev["gx"].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        index.copy_(src)
+        qf.qf_lora_plan(index, 3, c.plan)
+        c.u.zero_()
+        c.forward()
+        for w in c.ga + c.gb:
+            w.zero_()
+        c.backward()
+    index.fill_(-1)
+    for _ in range(2):
+        c.dev["y"].copy_(y0), c.dev["gx"].copy_(gx0)
+        graph.replay()
+    torch.cuda.synchronize()
+    c.u[300] = -7
+    c.u[:300][((c.index < 0) | (c.index > 2)).to(DEV)] = -7
+    c.check_forward()
+    c.check_backward()
