@@ -109,6 +109,9 @@ qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, 
     return e == cudaSuccess ? QF_OK : cuda_fail(e, "cudaLaunchKernelEx");
 }
 
+#ifndef QF_PROMO
+#define QF_PROMO CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+#endif
 // The tensor maps of a [rows, width] BF16 matrix.
 qf_status row_maps(qf::RowMaps* map, const void* p, int64_t rows, int64_t width, int64_t ld) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -129,7 +132,7 @@ qf_status row_maps(qf::RowMaps* map, const void* p, int64_t rows, int64_t width,
         const cuuint32_t box[2] = {64, i == 0 ? (cuuint32_t)qf::kBoxRows : 1};
         const CUresult r = encode(i == 0 ? &map->block : &map->row, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                                   const_cast<void*>(p), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, QF_PROMO,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
     }
@@ -159,9 +162,11 @@ qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, co
     }
     const int parts = parts_for(tiles, (depth + 255) / 256, 148 * QF_DOWN_SLOTS);
     if (tiles * parts > INT32_MAX) return fail(QF_ERR_SHAPE, "too many tokens for one launch");
-    return launch(qf::k_lora_down<MAXA>, dim3((unsigned)(tiles * parts)), qf::kTcThreads, qf::down_smem(wide), s,
-                  dim3(parts), A, P, map, (int)depth, (int)backward, parts, static_cast<uint16_t*>(u),
-                  wide);
+    // with an SM per CTA the ring takes what shared memory there is
+    const bool deep = tiles * parts <= 148 && wide <= 64;
+    return launch(deep ? qf::k_lora_down<MAXA, 8> : qf::k_lora_down<MAXA, QF_DOWN_STAGES>,
+                  dim3((unsigned)(tiles * parts)), qf::kTcThreads, qf::down_smem(deep ? 8 : QF_DOWN_STAGES, wide), s,
+                  dim3(parts), A, P, map, (int)depth, (int)backward, parts, static_cast<uint16_t*>(u), wide);
 }
 
 template <int MAXA, int KS>
@@ -169,10 +174,9 @@ qf_status up_ks(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, c
                 int64_t width, bool backward, void* y, int64_t ldy, cudaStream_t s) {
     const int64_t blocks = tiles * ((width + 255) / 256);
     if (blocks > INT32_MAX) return fail(QF_ERR_SHAPE, "tokens x width too large for one launch");
-    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), qf::kUpThreads,
-                  qf::UpShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16)), s,
-                  dim3(1), A, P, static_cast<const uint16_t*>(u), wide, (int)width, (int)backward,
-                  static_cast<uint16_t*>(y), ldy);
+    const size_t smem = qf::UpShape<KS>::smem((int)std::min<int64_t>(kLoraTile, (P.tokens + 15) / 16 * 16));
+    return launch(qf::k_lora_up<MAXA, KS>, dim3((unsigned)blocks), qf::kUpThreads, smem, s, dim3(1), A, P,
+                  static_cast<const uint16_t*>(u), wide, (int)width, (int)backward, static_cast<uint16_t*>(y), ldy);
 }
 template <int MAXA>
 qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* u, int wide, int64_t width,
@@ -218,11 +222,16 @@ int64_t tiles_of(const qf_lora_batch& c, int n) {
 }
 
 #ifndef QF_FEW_TOKENS
-#define QF_FEW_TOKENS 256       // at most so many tokens, and so many per adapter on average,
+#define QF_FEW_TOKENS 256
 #endif
-#ifndef QF_FEW_PER
-#define QF_FEW_PER 16           // take the one-launch kernel
-#endif
+// The one-launch kernel: few tokens per adapter (its clusters take 16 at a time), and either
+// no more than twice as many rows as columns or enough clusters to share the rows out.
+// Measured (one launch against two, us): 1 token 4096 x 4096 rank 16 5.4 / 8.0; 64 tokens of
+// 24 adapters, ranks 8 to 64, 4096 x 4096 10.3 / 13.0, 4096 x 14336 18.4 / 19.7, 14336 x
+// 4096 13.6 / 22.9; but 1 token 256 x 14336 7.8 / 6.0, rank 64 11.9 / 7.4.
+bool takes_few(const qf_lora_batch& c, int n, int64_t tiles) {
+    return c.tokens <= QF_FEW_TOKENS && c.tokens <= 16 * (int64_t)n && (c.rows <= 2 * c.cols || tiles >= 8);
+}
 template <int MAXA, int KS>
 qf_status few(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const qf_lora_batch& c, int wide,
               cudaStream_t s) {
@@ -238,7 +247,7 @@ qf_status apply(const qf_lora* l, int n, const qf_lora_batch& c, int wide, cudaS
     fill(A, l, n);
     const PlanView P = plan_view(c, n);
     const int64_t tiles = tiles_of(c, n);
-    if (c.tokens <= QF_FEW_TOKENS && c.tokens <= QF_FEW_PER * (int64_t)n) {
+    if (takes_few(c, n, tiles)) {
         if (wide <= 16) return few<MAXA, 1>(A, P, tiles, c, wide, s);
         if (wide <= 32) return few<MAXA, 2>(A, P, tiles, c, wide, s);
         if (wide <= 64) return few<MAXA, 4>(A, P, tiles, c, wide, s);

@@ -314,8 +314,11 @@ __device__ __forceinline__ void barrier_expect(uint64_t* bar, uint32_t bytes) {
 struct RowMaps {
     CUtensorMap block, row;
 };
-constexpr int kBoxRows = 32;
-__device__ __forceinline__ void load_rows32(uint32_t dst, const RowMaps* map, int col, int row, uint64_t* bar) {
+#ifndef QF_BOX_ROWS
+#define QF_BOX_ROWS 32
+#endif
+constexpr int kBoxRows = QF_BOX_ROWS, kBoxLanes = kBoxRows / 4;   // rows of a box; lanes whose gathers make one
+__device__ __forceinline__ void load_box(uint32_t dst, const RowMaps* map, int col, int row, uint64_t* bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(&map->block), "r"(col), "r"(row), "r"(smem_addr(bar))
                  : "memory");
@@ -423,23 +426,22 @@ struct TcPipe {
 // depth; the CTAs of a cluster share one tile's steps and add their sums through
 // distributed shared memory in rank order, so the result does not depend on timing.
 // Tokens that are neighbours, as a request's are, come in boxes of 32 rows; others four rows
-// a gather, one per lane (a box is one instruction for what takes eight gathers, and runs
-// at twice their rate).  Rows behind the tile's last only reach their own results.
+// a gather, one per lane (a gather's rows come at about half a box's rate).  Rows behind the tile's last only reach their own results.
 #ifndef QF_DOWN_STAGES
 #define QF_DOWN_STAGES 4
 #endif
 constexpr int kFactorCopiers = 64;
 __host__ __device__ constexpr uint32_t down_stage(int wide) { return kLoraTile * 128 + wide * 128; }
-constexpr size_t down_smem(int wide) {
-    const size_t pipe = size_t(QF_DOWN_STAGES) * down_stage(wide), red = size_t(kLoraTile) * (wide + 4) * 4;
+constexpr size_t down_smem(int stages, int wide) {
+    const size_t pipe = size_t(stages) * down_stage(wide), red = size_t(kLoraTile) * (wide + 4) * 4;
     return (pipe > red ? pipe : red) + 1024;
 }
-template <int MAXA>
+template <int MAXA, int ST>
 __global__ void __launch_bounds__(kTcThreads)
 k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const __grid_constant__ RowMaps zmap,
             int depth, int backward, int parts, uint16_t* __restrict__ u, int wide_max) {
     extern __shared__ unsigned char raw[];
-    __shared__ TcPipe<QF_DOWN_STAGES> pipe;
+    __shared__ TcPipe<ST> pipe;
     wait_previous_grid();
     let_next_grid_start();
     const Tile tile = tile_of(P, blockIdx.x / parts);     // parts = the cluster size
@@ -454,19 +456,19 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
     // a cluster's CTAs take every parts-th step: together they read whole stretches of a row
     const int part = blockIdx.x % parts, mine = ((depth + 63) / 64 - part + parts - 1) / parts;
     if (warp == 0) {
-        const int b = lane >> 3;                          // eight lanes to a box of 32 rows
+        const int b = lane / kBoxLanes;
         int row[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) row[i] = tile.token(min(4 * lane + i, tile.count - 1));
         const int live = min(kBoxRows, tile.count - b * kBoxRows);
-        const int top = __shfl_sync(0xFFFFFFFFu, row[0], lane & 24);
-        const int end = live > 0 ? tile.token(b * kBoxRows + live - 1) : 0;
+        const int top = __shfl_sync(0xFFFFFFFFu, row[0], lane & ~(kBoxLanes - 1));
+        const int end = __shfl_sync(0xFFFFFFFFu, row[3], lane | (kBoxLanes - 1));     // (repeats the tile's last)
         const bool dense = live > 0 && end - top == live - 1;           // (the plan keeps tokens in order)
         pipe.gather(mine, base, stage, (tile.count + kBoxRows - 1) / kBoxRows * kBoxRows * 128,
                     [&](int i, uint32_t to, uint64_t* full) {
             const int col = (part + i * parts) * 64;
             if (dense) {
-                if ((lane & 7) == 0) load_rows32(to + b * kBoxRows * 128, &zmap, col, top, full);
+                if (lane % kBoxLanes == 0) load_box(to + b * kBoxRows * 128, &zmap, col, top, full);
             } else if (live > 0) {
                 gather4(to + lane * 512, &zmap, col, make_int4(row[0], row[1], row[2], row[3]), full);
             }
@@ -548,7 +550,7 @@ template <int KS> struct UpShape {
     static constexpr int kPad = KS == 1 ? 16 : (KS * 16 + 31) / 32 * 32;
     static constexpr int kSteps = (kPad + 31) / 32;       // factor fragments
     static constexpr int kRow = 2 * kPad + (kPad > 16 ? 32 : 0);   // u's row: an odd multiple of 64 bytes
-    static constexpr size_t kRing = size_t(8) * kUpAhead * 2 * 512;
+    static constexpr size_t kRing = size_t(8) * 4 * 1024;  // four groups of 16 tokens, or steps of a walk, per warp
     __host__ __device__ static constexpr size_t u_bytes(int tokens) { return size_t(tokens) * kRow * 2; }
     __host__ __device__ static constexpr size_t smem(int tokens) { return u_bytes(tokens) + kRing; }
 };
@@ -561,7 +563,22 @@ struct UpColumns {
         const uint16_t* const b = backward ? ad.a : ad.b;
         const int ldf = backward ? (ad.rank + 15) / 16 * 16 : ad.rank;
         const bool vec = (ldf & 7) == 0 && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
-        const bool even = (ldf & 1) == 0 && (reinterpret_cast<uintptr_t>(b) & 3) == 0;
+        if (vec) {
+            // plain loads at clamped addresses: columns behind the width are not written, and
+            // positions behind the rank meet zeros of u (a conditional load would be waited
+            // for where its two outcomes join, one after the other)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = min(n0 + 8 * (g >> 1) + 2 * j + (g & 1), width - 1);
+                const uint16_t* const row = b + (int64_t)c * ldf;
+#pragma unroll
+                for (int k = 0; k < UpShape<KS>::kSteps; ++k) {
+                    const int r = pad == 16 ? 8 * (q & 1) : 32 * k + 8 * q;
+                    f[k][j] = *reinterpret_cast<const uint4*>(row + (r < ldf ? r : 0));
+                }
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int c = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
@@ -570,18 +587,9 @@ struct UpColumns {
                 const int r = pad == 16 ? 8 * (q & 1) : 32 * k + 8 * q;
                 const uint16_t* const p = b + (int64_t)c * ldf + r;
                 uint32_t w[4] = {0, 0, 0, 0};
-                if (c < width && r < ldf) {
-                    if (vec) {
-                        f[k][j] = *reinterpret_cast<const uint4*>(p);
-                        continue;
-                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (r + 2 * i >= ldf) continue;
-                        if (even) w[i] = *reinterpret_cast<const uint32_t*>(p + 2 * i);
-                        else w[i] = p[2 * i] | (r + 2 * i + 1 < ldf ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-                    }
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (c < width && r + i < ldf) w[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
                 f[k][j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
@@ -660,7 +668,7 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n0 = (int)(blockIdx.x % across) * 256 + warp * 32;
     const int wide = (ad.rank + 15) / 16 * 16, pad = up_pad(ad.rank), rows = min(kLoraTile, (P.tokens + 15) / 16 * 16);
     const uint32_t us = smem_addr(raw);
-    const uint32_t ys = us + (uint32_t)UpShape<KS>::u_bytes(rows) + warp * kUpAhead * 1024 + lane * 16;
+    const uint32_t ys = us + (uint32_t)UpShape<KS>::u_bytes(rows) + warp * 4 * 1024 + lane * 16;
     if (tid < kLoraTile) token[tid] = tile.token(min(tid, tile.count - 1));
     __syncthreads();
 #pragma unroll
@@ -696,18 +704,56 @@ k_lora_up(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const 
 // of them add the eight parts through distributed shared memory, each then does its eighth
 // of the columns, the factor and y of the next 32 columns always on the way; those of the
 // first before the sums are waited for, the rest of B's slice to L2 at the very start.
-constexpr int kFewParts = 8, kFewAhead = 2;
+// A warp walks over columns first, first + 256, ... below end, the factor and the
+// first 16 tokens' y of the next DEPTH - 1 steps on the way (the latency of a load is what
+// such a walk costs).  ready(): before u is read.
+template <int KS> __host__ __device__ constexpr int walk_depth() { return KS <= 2 ? 4 : 2; }
+template <int KS, typename READY>
+__device__ __forceinline__ void up_walk(const Adapter& ad, int pad, int count, const int* token,
+                                        uint32_t us, uint32_t ys, int first, int end, uint16_t* y, int64_t ldy,
+                                        READY ready) {
+    constexpr int DEPTH = walk_depth<KS>();
+    UpColumns<KS> C[DEPTH];
+    const auto fetch = [&](int d, int n) {
+        if (n < end) C[d].load_factor(ad, 0, n, end);
+        fetch_y<1>(0, count, token, ys + d * 1024, n, end, y, ldy);
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d) fetch(d, first + d * 256);
+    ready();
+    for (int n = first; n < end; n += DEPTH * 256) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int at = n + d * 256;
+            if (at >= end) break;
+            fetch((d + DEPTH - 1) % DEPTH, at + (DEPTH - 1) * 256);
+            for (int m = 0; 16 * m < count; ++m) {
+                if (m > 0) {                               // (not ahead: batches here have few tokens)
+                    fetch_y<1>(m, count, token, ys + d * 1024, at, end, y, ldy);
+                    cp_async_wait<0>();
+                }
+                float acc[4][4] = {};
+                up_products<KS>(C[d], pad, m, us, acc);
+                if (m == 0) cp_async_wait<DEPTH - 1>();
+                add_to_y<1>(m, count, token, ys + d * 1024, at, end, y, ldy, ad.scale, acc);
+            }
+        }
+    }
+    cp_async_wait<0>();
+}
+
+constexpr int kFewParts = 8;
 template <int KS> struct FewShape {
     static constexpr int kSum = KS * 16 + 4;              // floats per token of a partial u
     static constexpr size_t kPart = size_t(8) * 16 * kSum * 4;                // the warps' 16 tokens each
     static size_t all(int rows) { return size_t(rows) * kSum * 4; }           // the CTA's tokens
     static size_t smem(int rows) {
         return all(rows) + (kPart > UpShape<KS>::u_bytes(rows) ? kPart : UpShape<KS>::u_bytes(rows)) +
-               size_t(2) * 8 * kFewAhead * 1024;
+               UpShape<KS>::kRing;
     }
 };
 template <int MAXA, int KS>
-__global__ void __launch_bounds__(kUpThreads)
+__global__ void __launch_bounds__(kUpThreads, KS <= 4 ? 2 : 1)
 k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const uint16_t* __restrict__ x, int64_t ldx,
            int cols, uint16_t* __restrict__ u, int wide_max, int rows, uint16_t* y, int64_t ldy) {
     constexpr int SR = FewShape<KS>::kSum, UR = UpShape<KS>::kRow, NT = KS * 2;
@@ -722,8 +768,8 @@ k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const
     const int g = lane >> 2, q = lane & 3, wide = (ad.rank + 15) / 16 * 16, pad = up_pad(ad.rank);
     const int room = min(kLoraTile, (P.tokens + 15) / 16 * 16);
     unsigned char* at = raw;
-    const uint32_t ys = smem_addr(at) + warp * 2 * kFewAhead * 1024 + lane * 16;
-    at += 2 * 8 * kFewAhead * 1024;
+    const uint32_t ys = smem_addr(at) + warp * 4 * 1024 + lane * 16;
+    at += UpShape<KS>::kRing;
     float* const all = reinterpret_cast<float*>(at);
     at += (size_t)room * SR * 4;
     float* const part = reinterpret_cast<float*>(at);     // then u
@@ -739,26 +785,26 @@ k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const
         float acc[NT][4] = {};
         const uint16_t* const x0 = x + (int64_t)token[m + g] * ldx + 8 * q;
         const uint16_t* const x1 = x + (int64_t)token[m + g + 8] * ldx + 8 * q;
-#pragma unroll (KS == 1 ? 4 : 2)
-        for (int c = me * 8 + warp; c < steps; c += 8 * kFewParts) {
-            const bool in = 32 * c + 8 * q < cols;
+        const uint16_t* const a0 = ad.a + 8 * q;
+        const auto step = [&](int c, bool in) {            // (rows behind the rank repeat its last)
             const uint4 none = make_uint4(0, 0, 0, 0);
             const uint4 z0 = in ? *reinterpret_cast<const uint4*>(x0 + 32 * c) : none;
             const uint4 z1 = in ? *reinterpret_cast<const uint4*>(x1 + 32 * c) : none;
             uint4 f[NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int r = 8 * j + g;
-                f[j] = in && r < ad.rank ? *reinterpret_cast<const uint4*>(ad.a + (int64_t)r * cols + 32 * c + 8 * q) : none;
-            }
+            for (int j = 0; j < NT; ++j)
+                f[j] = in ? *reinterpret_cast<const uint4*>(a0 + (int64_t)min(8 * j + g, ad.rank - 1) * cols + 32 * c) : none;
             const uint32_t lo[4] = {z0.x, z1.x, z0.y, z1.y}, hi[4] = {z0.z, z1.z, z0.w, z1.w};
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                if (8 * j >= ad.rank) continue;
                 mma_bf16(acc[j], lo, f[j].x, f[j].y);
                 mma_bf16(acc[j], hi, f[j].z, f[j].w);
             }
-        }
+        };
+        int c = me * 8 + warp;
+#pragma unroll (KS == 1 ? 4 : 2)
+        for (; c < cols / 32; c += 8 * kFewParts) step(c, true);
+        if (c < steps) step(c, 32 * c + 8 * q < cols);
         float* const mine = part + warp * 16 * SR;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -777,56 +823,33 @@ k_lora_few(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const
                 s.z += v.z;
                 s.w += v.w;
             }
+            if (r + 1 >= ad.rank) s.y = 0.0f;
+            if (r + 2 >= ad.rank) s.z = 0.0f;
+            if (r + 3 >= ad.rank) s.w = 0.0f;
+            if (r >= ad.rank) s.x = 0.0f;
             *reinterpret_cast<float4*>(all + (m + t) * SR + r) = s;
         }
         __syncthreads();
     }
-    const int groups = (tile.count + 15) / 16;
-    const auto column = [&](int i) { return n0 + (warp + 8 * i) * 32; };
-    const auto ring = [&](int i) { return ys + (i & 1) * kFewAhead * 1024; };
-    const auto fetch = [&](int i) {
-        for (int m = 0; m < kFewAhead; ++m) fetch_y<kFewAhead>(m, tile.count, token, ring(i), column(i), n1, y, ldy);
-    };
-    UpColumns<KS> C;
-    C.load_factor(ad, 0, column(0), n1);
-    fetch(0);
-    cluster_sync();
-    for (int i = tid; i < tile.count * pad / 4; i += kUpThreads) {
-        const int t = i / (pad / 4), r = i % (pad / 4) * 4;
-        uint2 hi = make_uint2(0, 0), lo = make_uint2(0, 0);
-        if (r < wide) split_bf16(sum_cluster(all + t * SR + r, kFewParts), &hi, &lo);
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + r) * 2), "r"(hi.x), "r"(hi.y) : "memory");
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + pad + r) * 2), "r"(lo.x), "r"(lo.y)
-                     : "memory");
-        if (t % kFewParts == me && r < wide) {
-            uint16_t* const out = u + (int64_t)token[t] * 2 * wide_max + r;
-            *reinterpret_cast<uint2*>(out) = hi;
-            *reinterpret_cast<uint2*>(out + wide_max) = lo;
+    up_walk<KS>(ad, pad, tile.count, token, us, ys, n0 + warp * 32, n1, y, ldy, [&] {
+        cluster_sync();
+        for (int i = tid; i < tile.count * pad / 4; i += kUpThreads) {
+            const int t = i / (pad / 4), r = i % (pad / 4) * 4;
+            uint2 hi = make_uint2(0, 0), lo = make_uint2(0, 0);
+            if (r < wide) split_bf16(sum_cluster(all + t * SR + r, kFewParts), &hi, &lo);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + r) * 2), "r"(hi.x), "r"(hi.y)
+                         : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(us + (t * UR + pad + r) * 2), "r"(lo.x), "r"(lo.y)
+                         : "memory");
+            if (t % kFewParts == me && r < wide) {
+                uint16_t* const out = u + (int64_t)token[t] * 2 * wide_max + r;
+                *reinterpret_cast<uint2*>(out) = hi;
+                *reinterpret_cast<uint2*>(out + wide_max) = lo;
+            }
         }
-    }
-    asm volatile("barrier.cluster.arrive;" ::: "memory");  // done with the others' shared memory
-    __syncthreads();
-    for (int i = 0; column(i) < n1; ++i) {
-        UpColumns<KS> next;
-        const bool more = column(i + 1) < n1;
-        if (more) next.load_factor(ad, 0, column(i + 1), n1);
-        if (groups <= kFewAhead) {                          // the next columns' y fits beside these
-            fetch(i + 1);
-            cp_async_wait<kFewAhead>();
-        } else {
-            cp_async_wait<0>();
-        }
-        for (int m = 0; m < groups; ++m) {
-            float acc[4][4] = {};
-            up_products<KS>(C, pad, m, us, acc);
-            if (groups > kFewAhead && m > 0) cp_async_wait<kFewAhead - 1>();
-            add_to_y<kFewAhead>(m, tile.count, token, ring(i), column(i), n1, y, ldy, ad.scale, acc);
-            if (groups > kFewAhead) fetch_y<kFewAhead>(m + kFewAhead, tile.count, token, ring(i), column(i), n1, y, ldy);
-        }
-        if (groups > kFewAhead && more) fetch(i + 1);
-        if (more) C = next;
-    }
-    cp_async_wait<0>();
+        asm volatile("barrier.cluster.arrive;" ::: "memory");   // done with the others' shared memory
+        __syncthreads();
+    });
     asm volatile("barrier.cluster.wait;" ::: "memory");    // and they with this CTA's
 }
 
@@ -926,8 +949,8 @@ k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const _
     const int first = min(run.count, part * per), last = min(run.count, first + per);
     const int steps = (last - first + kGradTokens - 1) / kGradTokens;
     if (warp == 0) {
-        // a step's 64 tokens: two boxes per 64 columns where they are neighbours; otherwise
-        // sixteen gathers (tokens behind the slice as rows out of range: zeros)
+        // a step's 64 tokens: boxes where they are neighbours, otherwise gathers (tokens behind
+        // the slice as rows out of range: zeros)
         const RowMaps* const zmap = of_a ? &xmap : &gymap;
         const RowMaps* const wmap = of_a ? &vmap : &umap;
         const int blocks = 2 + (2 * wide_max + 63) / 64;       // of 64 columns: two of z, then w's
@@ -943,23 +966,17 @@ k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const _
         pipe.gather(steps, base, stage, blocks * kGradBlock, [&](int i, uint32_t to, uint64_t* full) {
             const int4 row = make_int4(next[0], next[1], next[2], next[3]);
             ids(i + 1);
-            // each half of the step's tokens by itself; both halves of the warp hold all of them
-            int top[2];
-            bool dense[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                top[h] = __shfl_sync(0xFFFFFFFFu, row.x, 8 * h);
-                dense[h] = __shfl_sync(0xFFFFFFFFu, row.w, 8 * h + 7) - top[h] == kBoxRows - 1 &&
-                           first + i * kGradTokens + (h + 1) * kBoxRows <= last;
-            }
-            const int mine = lane >> 3 & 1;
+            // each box by itself; both halves of the warp hold all of the step's tokens
+            const int box = (lane & 15) / kBoxLanes, top = __shfl_sync(0xFFFFFFFFu, row.x, lane & ~(kBoxLanes - 1));
+            const bool dense = __shfl_sync(0xFFFFFFFFu, row.w, lane | (kBoxLanes - 1)) - top == kBoxRows - 1 &&
+                               first + i * kGradTokens + (box + 1) * kBoxRows <= last;
             for (int b = lane >> 4; b < blocks; b += 2) {
                 const RowMaps* const map = b < 2 ? zmap : wmap;
                 const int col = b < 2 ? c0 + b * 64 : (b - 2) * 64;
-                if (!dense[mine])
+                if (!dense)
                     gather4(to + b * kGradBlock + (lane & 15) * 512, map, col, row, full);
-                else if ((lane & 7) == 0)
-                    load_rows32(to + b * kGradBlock + mine * kBoxRows * 128, map, col, top[mine], full);
+                else if (lane % kBoxLanes == 0)
+                    load_box(to + b * kGradBlock + box * kBoxRows * 128, map, col, top, full);
             }
         });
     } else if (warp == 1) {
