@@ -109,11 +109,8 @@ qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, 
     return e == cudaSuccess ? QF_OK : cuda_fail(e, "cudaLaunchKernelEx");
 }
 
-#ifndef QF_PROMO
-#define QF_PROMO CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-#endif
-// The tensor maps of a [rows, width] BF16 matrix.
-qf_status row_maps(qf::RowMaps* map, const void* p, int64_t rows, int64_t width, int64_t ld) {
+// The tensor map of a [rows, width] BF16 matrix.
+qf_status box_map(CUtensorMap* map, const void* p, int64_t rows, int64_t width, int64_t ld) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -127,16 +124,11 @@ qf_status row_maps(qf::RowMaps* map, const void* p, int64_t rows, int64_t width,
     }();
     if (encode == nullptr) return fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: not found in the driver");
     const cuuint64_t size[2] = {(cuuint64_t)width, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t step[2] = {1, 1};
-    for (int i = 0; i < 2; ++i) {
-        const cuuint32_t box[2] = {64, i == 0 ? (cuuint32_t)qf::kBoxRows : 1};
-        const CUresult r = encode(i == 0 ? &map->block : &map->row, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                                  const_cast<void*>(p), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  CU_TENSOR_MAP_SWIZZLE_128B, QF_PROMO,
-                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (r != CUDA_SUCCESS) return fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
-    }
-    return QF_OK;
+    const cuuint32_t box[2] = {64, (cuuint32_t)qf::kBoxRows}, step[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), size, stride, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QF_OK : fail(QF_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
 }
 
 #ifndef QF_DOWN_SLOTS
@@ -155,9 +147,9 @@ int parts_for(int64_t units, int64_t steps, int64_t slots) {
 template <int MAXA>
 qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, const void* z, int64_t ldz,
                int64_t depth, bool backward, void* u, int wide, cudaStream_t s) {
-    qf::RowMaps map{};
+    CUtensorMap map{};
     if (depth > 0) {
-        const qf_status st = row_maps(&map, z, P.tokens, depth, ldz);
+        const qf_status st = box_map(&map, z, P.tokens, depth, ldz);
         if (st != QF_OK) return st;
     }
     const int parts = parts_for(tiles, (depth + 255) / 256, 148 * QF_DOWN_SLOTS);
@@ -166,7 +158,7 @@ qf_status down(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, co
     const bool deep = tiles * parts <= 148 && wide <= 64;
     return launch(deep ? qf::k_lora_down<MAXA, 8> : qf::k_lora_down<MAXA, QF_DOWN_STAGES>,
                   dim3((unsigned)(tiles * parts)), qf::kTcThreads, qf::down_smem(deep ? 8 : QF_DOWN_STAGES, wide), s,
-                  dim3(parts), A, P, map, (int)depth, (int)backward, parts, static_cast<uint16_t*>(u), wide);
+                  dim3(parts), A, P, map, static_cast<const uint16_t*>(z), ldz, (int)depth, (int)backward, parts, static_cast<uint16_t*>(u), wide);
 }
 
 template <int MAXA, int KS>
@@ -190,21 +182,22 @@ qf_status up(const AdapterTable<MAXA>& A, const PlanView& P, int64_t tiles, cons
 template <int MAXA>
 qf_status grads(const qf::GradTable<MAXA>& G, const PlanView& P, int n, const qf_lora_batch& c, const void* v,
                 const void* gy, int64_t ldgy, int wide, bool beside, cudaStream_t s) {
-    qf::RowMaps x{}, y{}, vm{}, um{};
+    qf::GradMaps M{};
     qf_status st = QF_OK;
     if (c.tokens > 0) {
-        if (c.cols > 0) st = row_maps(&x, c.x, c.tokens, c.cols, c.ldx);
-        if (st == QF_OK && c.rows > 0) st = row_maps(&y, gy, c.tokens, c.rows, ldgy);
-        if (st == QF_OK) st = row_maps(&vm, v, c.tokens, 2 * wide, 2 * wide);
-        if (st == QF_OK) st = row_maps(&um, c.u, c.tokens, 2 * wide, 2 * wide);
+        if (c.cols > 0) st = box_map(&M.x, c.x, c.tokens, c.cols, c.ldx);
+        if (st == QF_OK && c.rows > 0) st = box_map(&M.gy, gy, c.tokens, c.rows, ldgy);
+        if (st == QF_OK) st = box_map(&M.v, v, c.tokens, 2 * wide, 2 * wide);
+        if (st == QF_OK) st = box_map(&M.u, c.u, c.tokens, 2 * wide, 2 * wide);
         if (st != QF_OK) return st;
     }
     const int64_t tiles = (c.cols + qf::kGradCols - 1) / qf::kGradCols + (c.rows + qf::kGradCols - 1) / qf::kGradCols;
     int parts = parts_for(tiles * n, (c.tokens / n + qf::kGradTokens - 1) / qf::kGradTokens, 148 * QF_GRAD_SLOTS);
     while (parts & (parts - 1)) --parts;          // its CTAs share a tile's 128 columns evenly
     return launch(qf::k_lora_grad<MAXA>, dim3((unsigned)tiles, n, parts), qf::kTcThreads,
-                  qf::grad_smem(wide), s, dim3(1, 1, parts), G, P, x, (int)c.cols, vm, y, (int)c.rows, um,
-                  wide, (int)beside);
+                  qf::grad_smem(wide), s, dim3(1, 1, parts), G, P, M, static_cast<const uint16_t*>(c.x),
+                  c.ldx, (int)c.cols, static_cast<const uint16_t*>(v), static_cast<const uint16_t*>(gy), ldgy,
+                  (int)c.rows, static_cast<const uint16_t*>(c.u), wide, (int)beside);
 }
 
 template <int MAXA>

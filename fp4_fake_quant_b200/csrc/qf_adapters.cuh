@@ -308,42 +308,32 @@ __device__ __forceinline__ void barrier_expect(uint64_t* bar, uint32_t bytes) {
     asm volatile("{ .reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1; }" ::"r"(smem_addr(bar)),
                  "r"(bytes) : "memory");
 }
-// A [rows, columns] BF16 matrix for TMA, 128-byte swizzle, zeros outside: in boxes of 64
-// columns by 32 rows (rows that are neighbours), and of 64 columns of single rows, four of
-// them per gather.
-struct RowMaps {
-    CUtensorMap block, row;
-};
-#ifndef QF_BOX_ROWS
-#define QF_BOX_ROWS 32
-#endif
-constexpr int kBoxRows = QF_BOX_ROWS, kBoxLanes = kBoxRows / 4;   // rows of a box; lanes whose gathers make one
-__device__ __forceinline__ void load_box(uint32_t dst, const RowMaps* map, int col, int row, uint64_t* bar) {
+// A [rows, columns] BF16 matrix for TMA: boxes of 64 columns by 32 rows, 128-byte swizzle,
+// zeros outside.
+constexpr int kBoxRows = 32;
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int col, int row, uint64_t* bar) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(&map->block), "r"(col), "r"(row), "r"(smem_addr(bar))
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(smem_addr(bar))
                  : "memory");
 }
-__device__ __forceinline__ void gather4(uint32_t dst, const RowMaps* map, int col, int4 row, uint64_t* bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(&map->row), "r"(col), "r"(row.x),
-                 "r"(row.y), "r"(row.z), "r"(row.w), "r"(smem_addr(bar)) : "memory");
-}
 
-// One CTA's product in TMEM.  Warp 0 gathers rows by TMA, warp 1's first lane issues the
-// MMAs, further warps may copy the other operand by cp.async; all four read the result.
-// `full` of a stage: warp 0's expected bytes and the copiers' arrivals; `empty`: its MMAs
-// have committed.
-constexpr int kTcThreads = 128;
+// One CTA's product in TMEM.  Warp 0 brings boxes of neighbouring rows by TMA, warp 1's
+// first lane issues the MMAs, warps 2 and 3 copy what is not a box by cp.async; all four
+// read the result.  (TMA's tile::gather4 for rows that are not neighbours took about 57
+// cycles a gather, 1800 for a step of 128 rows against 250 of cp.async: 8191 tokens of 37
+// requests x 14336 took 77 us with it.)  `full` of a stage: warp 0's expected bytes and the
+// copiers' arrivals; `empty`: its MMAs have committed.
+constexpr int kTcThreads = 128, kCopiers = 64;
 template <int ST>
 struct TcPipe {
     uint64_t full[ST], empty[ST], done;
     uint32_t tmem;
     int dead;
-    __device__ __forceinline__ void start(int cols, int arrivals) {     // every thread; ends with a barrier
+    __device__ __forceinline__ void start(int cols) {                   // every thread; ends with a barrier
         if (threadIdx.x == 0) {
 #pragma unroll
             for (int i = 0; i < ST; ++i) {
-                barrier_init(&full[i], arrivals);
+                barrier_init(&full[i], 1 + kCopiers);
                 barrier_init(&empty[i], 1);
             }
             barrier_init(&done, 1);
@@ -355,16 +345,18 @@ struct TcPipe {
         __syncthreads();
         after_sync();
     }
-    // warp 0: FETCH(i, stage base, full barrier) issues one lane's part of step i
-    template <typename FETCH>
-    __device__ __forceinline__ void gather(int steps, uint32_t base, uint32_t stage, uint32_t bytes, FETCH fetch) {
+    // warp 0: BYTES(i) of step i come as boxes; FETCH(i, stage base, full barrier) issues one
+    // lane's part of them
+    template <typename BYTES, typename FETCH>
+    __device__ __forceinline__ void boxes(int steps, uint32_t base, uint32_t stage, BYTES bytes, FETCH fetch) {
         for (int i = 0; i < steps; ++i) {
             const int s = i % ST;
+            const uint32_t n = bytes(i);
             if (i >= ST && !barrier_wait(&empty[s], (i / ST - 1) & 1)) {
                 dead = 1;
                 return;
             }
-            if (threadIdx.x == 0) barrier_expect(&full[s], bytes);
+            if (threadIdx.x == 0) barrier_expect(&full[s], n);
             __syncwarp();
             fetch(i, base + s * stage, &full[s]);
         }
@@ -425,12 +417,11 @@ struct TcPipe {
 // A CTA takes one tile (128 rows = the MMA's M, the rank is its N) and steps of 64 columns of
 // depth; the CTAs of a cluster share one tile's steps and add their sums through
 // distributed shared memory in rank order, so the result does not depend on timing.
-// Tokens that are neighbours, as a request's are, come in boxes of 32 rows; others four rows
-// a gather, one per lane (a gather's rows come at about half a box's rate).  Rows behind the tile's last only reach their own results.
+// Rows behind the tile's last are not loaded, or are others': what lies there only reaches
+// its own results.
 #ifndef QF_DOWN_STAGES
 #define QF_DOWN_STAGES 4
 #endif
-constexpr int kFactorCopiers = 64;
 __host__ __device__ constexpr uint32_t down_stage(int wide) { return kLoraTile * 128 + wide * 128; }
 constexpr size_t down_smem(int stages, int wide) {
     const size_t pipe = size_t(stages) * down_stage(wide), red = size_t(kLoraTile) * (wide + 4) * 4;
@@ -438,10 +429,11 @@ constexpr size_t down_smem(int stages, int wide) {
 }
 template <int MAXA, int ST>
 __global__ void __launch_bounds__(kTcThreads)
-k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const __grid_constant__ RowMaps zmap,
-            int depth, int backward, int parts, uint16_t* __restrict__ u, int wide_max) {
+k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, const __grid_constant__ CUtensorMap zmap,
+            const uint16_t* __restrict__ z, int64_t ldz, int depth, int backward, int parts, uint16_t* __restrict__ u, int wide_max) {
     extern __shared__ unsigned char raw[];
     __shared__ TcPipe<ST> pipe;
+    __shared__ int token[kLoraTile];
     wait_previous_grid();
     let_next_grid_start();
     const Tile tile = tile_of(P, blockIdx.x / parts);     // parts = the cluster size
@@ -452,26 +444,22 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, stage = down_stage(wide);
     float* const red = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
     const int RW = wide + 4;
-    pipe.start(cols, 1 + kFactorCopiers);
+    token[tid] = tile.token(min(tid, tile.count - 1));
+    pipe.start(cols);
     // a cluster's CTAs take every parts-th step: together they read whole stretches of a row
     const int part = blockIdx.x % parts, mine = ((depth + 63) / 64 - part + parts - 1) / parts;
+    // which of the tile's four boxes of rows are neighbours (the plan keeps tokens in order)
+    const auto rows_of = [&](int b) { return min(kBoxRows, tile.count - b * kBoxRows); };
+    const auto dense = [&](int b) {
+        const int n = rows_of(b);
+        return n > 0 && token[b * kBoxRows + n - 1] - token[b * kBoxRows] == n - 1;
+    };
     if (warp == 0) {
-        const int b = lane / kBoxLanes;
-        int row[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) row[i] = tile.token(min(4 * lane + i, tile.count - 1));
-        const int live = min(kBoxRows, tile.count - b * kBoxRows);
-        const int top = __shfl_sync(0xFFFFFFFFu, row[0], lane & ~(kBoxLanes - 1));
-        const int end = __shfl_sync(0xFFFFFFFFu, row[3], lane | (kBoxLanes - 1));     // (repeats the tile's last)
-        const bool dense = live > 0 && end - top == live - 1;           // (the plan keeps tokens in order)
-        pipe.gather(mine, base, stage, (tile.count + kBoxRows - 1) / kBoxRows * kBoxRows * 128,
-                    [&](int i, uint32_t to, uint64_t* full) {
-            const int col = (part + i * parts) * 64;
-            if (dense) {
-                if (lane % kBoxLanes == 0) load_box(to + b * kBoxRows * 128, &zmap, col, top, full);
-            } else if (live > 0) {
-                gather4(to + lane * 512, &zmap, col, make_int4(row[0], row[1], row[2], row[3]), full);
-            }
+        const bool mine_dense = lane < 4 && dense(lane);
+        const int top = token[32 * (lane & 3)];
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine_dense)) * kBoxRows * 128;
+        pipe.boxes(mine, base, stage, [&](int) { return bytes; }, [&](int i, uint32_t to, uint64_t* full) {
+            if (mine_dense) load_box(to + lane * kBoxRows * 128, &zmap, (part + i * parts) * 64, top, full);
         });
     } else if (warp == 1) {
         const uint32_t shape = mma_shape(wide, false);
@@ -485,12 +473,24 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
     } else {
         const int c = tid & 7, r0 = (tid - 64) >> 3;      // 16-byte column, first of every 8th row
         const uint16_t* const f = (backward ? ad.b : ad.a) + (int64_t)r0 * depth;
-        const uint32_t at = kLoraTile * 128 + r0 * 128 + ((c ^ r0) << 4);
+        const uint32_t at = r0 * 128 + ((c ^ r0) << 4);
+        int loose = 0;                                    // boxes to copy row by row
+        for (int b = 0; b < 4; ++b) loose |= (rows_of(b) > 0 && !dense(b)) << b;
         pipe.copy(mine, base, stage, [&](int i, uint32_t to) {
             const int k0 = (part + i * parts) * 64 + c * 8;
+            const bool in = k0 < depth;
+            const int off = in ? k0 : 0;                  // (a zero-filled copy reads nothing)
+            for (int b = 0; b < 4; ++b)
+                if (loose >> b & 1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = b * kBoxRows + r0 + 8 * k;
+                        cp_async16(to + b * kBoxRows * 128 + at + k * 1024, z + (int64_t)token[r] * ldz + off, in);
+                    }
+                }
             for (int k = 0; k < wide; k += 8) {
-                const bool in = k0 < depth && r0 + k < ad.rank;
-                cp_async16(to + at + k * 128, in ? f + (int64_t)k * depth + k0 : ad.a, in);
+                const bool live = in && r0 + k < ad.rank;
+                cp_async16(to + kLoraTile * 128 + at + k * 128, live ? f + (int64_t)k * depth + off : ad.a, live);
             }
         });
     }
@@ -918,11 +918,14 @@ constexpr size_t grad_smem(int wide) {
     const size_t pipe = size_t(QF_GRAD_STAGES) * grad_stage(wide), red = size_t(wide) * (kGradCols + 4) * 4;
     return (pipe > red ? pipe : red) + 1024;
 }
+struct GradMaps {
+    CUtensorMap x, v, gy, u;
+};
 template <int MAXA>
 __global__ void __launch_bounds__(kTcThreads)
-k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const __grid_constant__ RowMaps xmap,
-            int cols, const __grid_constant__ RowMaps vmap, const __grid_constant__ RowMaps gymap, int rows,
-            const __grid_constant__ RowMaps umap, int wide_max, int beside) {
+k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const __grid_constant__ GradMaps M,
+            const uint16_t* __restrict__ x, int64_t ldx, int cols, const uint16_t* v,
+            const uint16_t* __restrict__ gy, int64_t ldgy, int rows, const uint16_t* u, int wide_max, int beside) {
     constexpr int RS = kGradCols + 4;
     extern __shared__ unsigned char raw[];
     __shared__ TcPipe<QF_GRAD_STAGES> pipe;
@@ -944,40 +947,31 @@ k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const _
     const int rank = A.rank[adapter], wide = (rank + 15) / 16 * 16, tc = tmem_cols(2 * wide_max);
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u, stage = grad_stage(wide_max);
     float* const red = reinterpret_cast<float*>(raw + (base - smem_addr(raw)));
-    pipe.start(tc, 1);
+    pipe.start(tc);
     const int per = ((run.count + parts - 1) / parts + kGradTokens - 1) / kGradTokens * kGradTokens;
     const int first = min(run.count, part * per), last = min(run.count, first + per);
     const int steps = (last - first + kGradTokens - 1) / kGradTokens;
+    // a step's tokens are two boxes of rows; a box whose tokens are neighbours, all of them
+    // inside the slice, comes by TMA; of others the tokens behind the slice are zeros
+    const auto top_of = [&](int i, int h, int* top) {
+        const int t = first + i * kGradTokens + h * kBoxRows;
+        *top = t < last ? run.token(t) : 0;
+        return t + kBoxRows <= last && run.token(t + kBoxRows - 1) - *top == kBoxRows - 1;
+    };
+    const int blocks = 2 + (2 * wide_max + 63) / 64;          // of 64 columns: two of z, then w's
     if (warp == 0) {
-        // a step's 64 tokens: boxes where they are neighbours, otherwise gathers (tokens behind
-        // the slice as rows out of range: zeros)
-        const RowMaps* const zmap = of_a ? &xmap : &gymap;
-        const RowMaps* const wmap = of_a ? &vmap : &umap;
-        const int blocks = 2 + (2 * wide_max + 63) / 64;       // of 64 columns: two of z, then w's
-        int next[4];
-        auto ids = [&](int i) {                                // a lane's four tokens of a step
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = first + i * kGradTokens + 4 * (lane & 15) + k;
-                next[k] = t < last ? run.token(t) : P.tokens;
-            }
-        };
-        ids(0);
-        pipe.gather(steps, base, stage, blocks * kGradBlock, [&](int i, uint32_t to, uint64_t* full) {
-            const int4 row = make_int4(next[0], next[1], next[2], next[3]);
-            ids(i + 1);
-            // each box by itself; both halves of the warp hold all of the step's tokens
-            const int box = (lane & 15) / kBoxLanes, top = __shfl_sync(0xFFFFFFFFu, row.x, lane & ~(kBoxLanes - 1));
-            const bool dense = __shfl_sync(0xFFFFFFFFu, row.w, lane | (kBoxLanes - 1)) - top == kBoxRows - 1 &&
-                               first + i * kGradTokens + (box + 1) * kBoxRows <= last;
-            for (int b = lane >> 4; b < blocks; b += 2) {
-                const RowMaps* const map = b < 2 ? zmap : wmap;
-                const int col = b < 2 ? c0 + b * 64 : (b - 2) * 64;
-                if (!dense)
-                    gather4(to + b * kGradBlock + (lane & 15) * 512, map, col, row, full);
-                else if (lane % kBoxLanes == 0)
-                    load_box(to + b * kGradBlock + box * kBoxRows * 128, map, col, top, full);
-            }
+        const CUtensorMap* const zmap = of_a ? &M.x : &M.gy;
+        const CUtensorMap* const wmap = of_a ? &M.v : &M.u;
+        int top = 0;
+        bool dense = false;
+        pipe.boxes(steps, base, stage, [&](int i) {
+            dense = top_of(i, lane & 1, &top);
+            return __popc(__ballot_sync(0xFFFFFFFFu, dense) & 3) * blocks * kBoxRows * 128;
+        }, [&](int, uint32_t to, uint64_t* full) {
+            const int b = lane >> 1;
+            if (dense && b < blocks)
+                load_box(to + b * kGradBlock + (lane & 1) * kBoxRows * 128, b < 2 ? zmap : wmap,
+                         b < 2 ? c0 + b * 64 : (b - 2) * 64, top, full);
         });
     } else if (warp == 1) {
         const uint32_t shape = mma_shape(2 * wide_max, true);
@@ -988,6 +982,30 @@ k_lora_grad(const __grid_constant__ GradTable<MAXA> A, const PlanView P, const _
                     mma_tc(pipe.tmem, operand(from + 2048 * k, kGradBlock, 1024),
                            operand(from + 2 * kGradBlock + 2048 * k, kGradBlock, 1024), shape, i > 0 || k > 0);
             });
+    } else {
+        const uint16_t* const z = of_a ? x : gy;
+        const uint16_t* const w = of_a ? v : u;
+        const int64_t ldz = of_a ? ldx : ldgy;
+        const int c = tid & 7, r0 = (tid - 64) >> 3;          // 16-byte column of a block, every 8th row
+        pipe.copy(steps, base, stage, [&](int i, uint32_t to) {
+            for (int h = 0; h < 2; ++h) {
+                int top;
+                if (top_of(i, h, &top)) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = h * kBoxRows + r0 + 8 * k, t = first + i * kGradTokens + r;
+                    const bool in = t < last;
+                    const int64_t id = in ? run.token(t) : 0;
+                    const uint32_t at = to + r * 128 + ((c ^ r0) << 4);
+                    for (int b = 0; b < blocks; ++b) {
+                        const int col = (b < 2 ? c0 + b * 64 : (b - 2) * 64) + c * 8;
+                        const bool live = in && col < (b < 2 ? depth : 2 * wide_max);
+                        const uint16_t* const p = b < 2 ? z + id * ldz : w + id * 2 * wide_max;
+                        cp_async16(at + b * kGradBlock, live ? p + col : z, live);
+                    }
+                }
+            }
+        });
     }
     __syncwarp();
     const bool good = pipe.result();
