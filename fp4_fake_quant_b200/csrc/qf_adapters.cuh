@@ -362,11 +362,13 @@ struct TcPipe {
         }
     }
     // copiers: FETCH(i, stage base) issues one thread's cp.async of step i; a step's copies
-    // are waited for, and fenced for the tensor core's proxy, one step later (the later, the
-    // closer each MMA comes to waiting for those before it to free a stage)
+    // are waited for, and fenced for the tensor core's proxy, ST - 2 steps later.  (Sooner,
+    // fewer copies are in flight; later, each MMA waits for the one before it to free the
+    // stage whose copies are issued before its own are fenced.)
     template <typename FETCH>
     __device__ __forceinline__ void copy(int steps, uint32_t base, uint32_t stage, FETCH fetch) {
-        for (int i = 0; i < steps + 1; ++i) {
+        constexpr int LAG = ST - 2;
+        for (int i = 0; i < steps + LAG; ++i) {
             if (i < steps) {
                 if (i >= ST && !barrier_wait(&empty[i % ST], (i / ST - 1) & 1)) {
                     dead = 1;
@@ -375,10 +377,10 @@ struct TcPipe {
                 fetch(i, base + (i % ST) * stage);
             }
             cp_async_commit();
-            if (i >= 1) {
-                cp_async_wait<1>();
+            if (i >= LAG) {
+                cp_async_wait<LAG>();
                 writes_to_async();
-                barrier_arrive(&full[(i - 1) % ST]);
+                barrier_arrive(&full[(i - LAG) % ST]);
             }
         }
         cp_async_wait<0>();
