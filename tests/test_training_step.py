@@ -1,0 +1,118 @@
+"""The operators of a training step used together, as a run uses them: LoRA-QAD on an NVFP4
+base (fake-quant, shared projection, adapters forward and backward, gradient norm, AdamW on
+the factors, the merge of the trained adapter), and full-parameter QAT (AdamW's tie-group
+amax feeds the next fake-quant)."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_fake_quant_b200 as qf
+from test_adamw import step32
+
+DEV = "cuda:0"
+H = 2.0 ** -8
+
+
+def _randn(gen, *shape, std=1.0):
+    return (torch.randn(*shape, generator=gen) * std).bfloat16().to(DEV)
+
+
+@pytest.mark.gpu
+def test_lora_qad_steps():
+    """Two steps of two adapters on a quantized base.  Each stage is checked on the device's own
+    inputs of that stage: y and gx within their BF16 roundings, the gradients' norm, the
+    factors bit for bit the documented AdamW step of the gradients."""
+    gen = torch.Generator().manual_seed(0)
+    rows, cols, tokens, ranks = 96, 256, 300, [16, 8]
+    w = _randn(gen, rows, cols, std=0.02)
+    wq, codes, scales = qf.alloc_outputs("nvfp4", w)
+    qf.qf_amax_fakequant([w], [wq], [codes], [scales], [0], torch.empty(1, device=DEV))
+    adapters = [(_randn(gen, rows, r, std=0.05), _randn(gen, r, cols, std=cols ** -0.5), 2.0) for r in ranks]
+    factors = [t for b, a, _ in adapters for t in (b, a)]
+    states = [qf.alloc_adamw_state(p) for p in factors]
+    ga, gb = ([torch.empty_like(x[i]) for x in adapters] for i in (1, 0))
+    grads = [g for pair in zip(gb, ga) for g in pair]
+    norm, step = torch.empty(2, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    ws, u = qf.alloc_grad_norm_workspace(DEV), qf.alloc_lora_u(tokens, adapters)
+    for t in (1, 2):
+        x, target = _randn(gen, tokens, cols), _randn(gen, tokens, rows)
+        index = torch.randint(-1, 2, (tokens,), generator=gen, dtype=torch.int32)
+        plan = qf.qf_lora_plan(index.to(DEV), 2)
+        y = x @ wq.t()
+        base = y.double()
+        qf.qf_lora_apply(x, adapters, y, u, plan=plan)
+        gy = y - target
+        gx = gy @ wq
+        gx0 = gx.double()
+        qf.qf_lora_apply_backward(x, gy, adapters, u, gx, ga, gb, plan=plan)
+        qf.qf_grad_norm(grads, norm, max_norm=0.5, step_tensor=step, workspace=ws)
+        before = [p.float().cpu().numpy() for p in factors]
+        moments = [(m.cpu().numpy(), v.cpu().numpy()) for m, v, *_ in states]
+        old = [(b.double(), a.double(), s) for b, a, s in adapters]
+        qf.qf_adamw(factors, grads, [s[0] for s in states], [s[1] for s in states], lr=1e-3,
+                    step_tensor=step, grad_scale=norm[1:], weight_decay=0.01)
+        torch.cuda.synchronize()
+        for i, (b, a, s) in enumerate(old):
+            r = (index == i).nonzero().view(-1).to(DEV)
+            d = s * (x[r].double() @ a.t()) @ b.t()
+            assert ((y[r].double() - base[r] - d).abs() <= H * (base[r] + d).abs() + 1e-4 * d.abs().max()).all()
+            d = s * (gy[r].double() @ b) @ a
+            assert ((gx[r].double() - gx0[r] - d).abs() <= H * (gx0[r] + d).abs() + 1e-4 * d.abs().max()).all()
+            want = s * (gy[r].double() @ b).t() @ x[r].double()
+            assert ((ga[i].double() - want).abs() <= H * want.abs() + 1e-4 * want.abs().max()).all()
+        total = sum(float(g.double().square().sum()) for g in grads) ** 0.5
+        assert abs(norm[0].item() - total) <= total * 2.0 ** -23 and step.item() == t
+        for p, g, b, (m, v), st in zip(factors, grads, before, moments, states):
+            want = step32(b.ravel(), g.float().cpu().numpy().ravel(), m.ravel(), v.ravel(), t,
+                          norm[1].item(), lr=1e-3, betas=(0.9, 0.999), weight_decay=0.01, p16=True)
+            assert np.array_equal(p.float().cpu().numpy().ravel(), want[0])
+            assert np.array_equal(st[0].cpu().numpy().ravel(), want[1])
+            assert np.array_equal(st[1].cpu().numpy().ravel(), want[2])
+    # the merge of the trained adapter gives the projection the adapter gave beside it
+    b, a, s = adapters[0]
+    x, merged = _randn(gen, 64, cols), torch.empty_like(w)
+    qf.qf_lora_merge([w], [(b, a, s)], [merged])
+    beside = torch.zeros(64, rows, dtype=torch.bfloat16, device=DEV)
+    qf.qf_lora_apply(x, [(b, a, s)], beside)
+    want = x.double() @ (merged.double() - w.double()).t()
+    # each merged weight is within half a BF16 step of W + s B A
+    tol = H * (x.double().abs() @ (merged.double().abs() + w.double().abs()).t() + beside.double().abs()) + 1e-6
+    assert ((beside.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_steps_amax_feeds_the_next_forward_pass(bits):
+    """FP32 masters in two tie groups: fake-quant on the amax that AdamW left gives the bytes of
+    a fresh amax and fake-quant, step after step, also from a captured step."""
+    gen = torch.Generator().manual_seed(1)
+    shapes, groups = [(64, 256), (32, 256), (48, 512)], [0, 0, 1]
+    ps = [(torch.randn(*s, generator=gen) * 0.02).to(DEV) for s in shapes]
+    grads = [torch.empty(*s, dtype=torch.bfloat16, device=DEV) for s in shapes]
+    states = [qf.alloc_adamw_state(p, bits) for p in ps]
+    amax, step = torch.empty(2, device=DEV), torch.zeros(1, dtype=torch.int64, device=DEV)
+    norm, ws = torch.empty(2, device=DEV), qf.alloc_grad_norm_workspace(DEV)
+    qf.qf_amax_tied(ps, groups, amax)
+    outs = [qf.alloc_outputs("nvfp4", p) for p in ps]
+    more = dict(m_scales=[s[2] for s in states], v_scales=[s[3] for s in states]) if bits == 8 else {}
+
+    def one():
+        qf.qf_fakequant("nvfp4", ps, *[[o[i] for o in outs] for i in range(3)], groups, amax)
+        qf.qf_grad_norm(grads, norm, max_norm=1.0, step_tensor=step, workspace=ws)
+        qf.qf_adamw(ps, grads, [s[0] for s in states], [s[1] for s in states], lr=1e-2, step_tensor=step,
+                    grad_scale=norm[1:], groups=groups, group_amax=amax, **more)
+    graph = None
+    for t in range(4):
+        for g in grads:
+            g.copy_((torch.randn(*g.shape, generator=gen) * 1e-2).bfloat16())
+        if t == 2:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+                one()
+        fresh, want = torch.empty(2, device=DEV), [qf.alloc_outputs("nvfp4", p) for p in ps]
+        qf.qf_amax_fakequant(ps, *[[o[i] for o in want] for i in range(3)], groups, fresh)
+        graph.replay() if graph else one()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o, w))
+    assert step.item() == 4
