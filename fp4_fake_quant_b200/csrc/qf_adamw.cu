@@ -93,9 +93,7 @@ qf_status adam_launch(const qf_param* t, int n, const AdamScalars& h, float* ama
     P.amax = reinterpret_cast<uint32_t*>(amax);
     const int64_t want = (units + kAdamThreads / 32 - 1) / (kAdamThreads / 32);
     const int64_t cap = (int64_t)L.sms * L.per_sm * QF_ADAM_WAVES;
-    qf::k_adamw<PT, GT, ST, MAXT><<<(unsigned)std::min(want, cap), kAdamThreads, 0, s>>>(P);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? QF_OK : cuda_fail(e, "kernel launch");
+    return launch(qf::k_adamw<PT, GT, ST, MAXT>, dim3((unsigned)std::min(want, cap)), kAdamThreads, 0, s, dim3(1), P);
 }
 
 // The tensors in launches of at most kLargeP and kParamMaxUnits (empty ones are dropped).
@@ -152,9 +150,7 @@ qf_status norm_launch(const qf_param* t, int n, double max_norm, float* out, int
     P.last = last;
     const int64_t want = std::max<int64_t>(1, (units + kAdamThreads / 32 - 1) / (kAdamThreads / 32));
     const int64_t cap = std::min<int64_t>((int64_t)L.sms * L.per_sm, qf::kNormMaxGrid);
-    qf::k_grad_norm<GT, MAXT><<<(unsigned)std::min(want, cap), kAdamThreads, 0, s>>>(P);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? QF_OK : cuda_fail(e, "kernel launch");
+    return launch(qf::k_grad_norm<GT, MAXT>, dim3((unsigned)std::min(want, cap)), kAdamThreads, 0, s, dim3(1), P);
 }
 
 template <typename GT>

@@ -329,6 +329,8 @@ k_adamw(const __grid_constant__ ParamTable<MAXT> P) {
     constexpr bool S8 = sizeof(ST) == 1;
     constexpr bool kAhead = S8 && QF_ADAM_PREFETCH;
     __shared__ float sh[2];
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // gradients and scalars come from kernels before
+    asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31;
     const AdamScalars& h = P.h;
     float ss = h.ss, rs2 = h.rs2;
@@ -550,6 +552,8 @@ __global__ void __launch_bounds__(kAdamThreads) k_grad_norm(const __grid_constan
     constexpr int kUnit = 32 * kVec * kNormVecs;
     __shared__ double sh[kAdamThreads / 32];
     __shared__ bool is_last;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t stride = (int64_t)gridDim.x * (kAdamThreads / 32);
     double acc[4] = {0.0, 0.0, 0.0, 0.0};

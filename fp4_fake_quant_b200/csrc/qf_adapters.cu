@@ -80,35 +80,6 @@ qf_status check_u(const qf_lora_batch& c) {
     return QF_OK;
 }
 
-// One launch as a programmatic dependent of the kernel before it, in clusters.  Every kernel
-// here waits for that one's end before it touches memory that may depend on it, and before
-// it lets the next one start.
-template <typename K, typename... Args>
-qf_status launch(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, dim3 cluster, Args... args) {
-    Shape shape;                                   // (also raises the shared-memory limit once)
-    const qf_status st = shape_of(kernel, threads, smem, &shape);
-    if (st != QF_OK) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    int k = 0;
-    attr[k].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[k++].val.programmaticStreamSerializationAllowed = 1;
-    if (cluster.x * cluster.y * cluster.z > 1) {
-        attr[k].id = cudaLaunchAttributeClusterDimension;
-        attr[k].val.clusterDim.x = cluster.x;
-        attr[k].val.clusterDim.y = cluster.y;
-        attr[k++].val.clusterDim.z = cluster.z;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = k;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e == cudaSuccess ? QF_OK : cuda_fail(e, "cudaLaunchKernelEx");
-}
-
 // The tensor map of a [rows, width] BF16 matrix.
 qf_status box_map(CUtensorMap* map, const void* p, int64_t rows, int64_t width, int64_t ld) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
