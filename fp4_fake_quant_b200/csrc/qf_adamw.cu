@@ -149,7 +149,7 @@ qf_status norm_launch(const qf_param* t, int n, double max_norm, float* out, int
     P.first = first;
     P.last = last;
     const int64_t want = std::max<int64_t>(1, (units + kAdamThreads / 32 - 1) / (kAdamThreads / 32));
-    const int64_t cap = std::min<int64_t>((int64_t)L.sms * L.per_sm, qf::kNormMaxGrid);
+    const int64_t cap = std::min<int64_t>((int64_t)L.sms * L.per_sm * 8, qf::kNormMaxGrid);
     return launch(qf::k_grad_norm<GT, MAXT>, dim3((unsigned)std::min(want, cap)), kAdamThreads, 0, s, dim3(1), P);
 }
 

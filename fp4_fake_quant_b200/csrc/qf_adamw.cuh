@@ -33,7 +33,7 @@ constexpr int kParamBlock = 256;        // elements behind one 8-bit scale
 constexpr int kAdamThreads = 256;
 constexpr int kSmallP = 8;              // descriptor table sizes; 352 x 88 B = 31 KB of the
 constexpr int kLargeP = 352;            // 32 KB of kernel parameters
-constexpr int kNormMaxGrid = 2048;
+constexpr int kNormMaxGrid = 8192;
 
 struct DevParam {
     void* p;
@@ -509,14 +509,13 @@ k_adamw(const __grid_constant__ ParamTable<MAXT> P) {
 
 // ---------------------------------------------------------------- global gradient norm
 //
-// norm = sqrt(sum over every element of every tensor of g^2), the sum in binary64.  The
-// binary64 pipe takes one fused multiply-add per element; the conversion to binary64
-// would cost the slow conversion pipe instead, so it is done on the bits: shift the
-// mantissa, rebias the exponent.  Subnormals come out as if normal, below 2^-126 (their
-// squares are below 2^-252, nothing beside any FP32 norm); infinities and NaN come out at
-// 2^128 or above, so a gradient that holds one gives norm >= 2^128 = +inf in FP32, which
-// is the mark of a step to skip.
-// Bound: HBM, one read of g.  Each warp keeps 4 vectors of 16 bytes per lane in flight.
+// norm = sqrt(sum over every element of every tensor of g^2), the sum in binary64: one
+// conversion (16 a cycle and SM, enough for 6.5 TB/s of either type) and one fused
+// multiply-add per element.  A sum that is not finite, or a norm above FP32, gives +inf, the
+// mark of a step to skip.
+// Bound: HBM, one read of g.  Each warp keeps 4 vectors of 16 bytes per lane in flight; eight
+// CTAs per resident slot.  226M FP32 gradients: 153 us, 5.93 TB/s (a persistent grid 159;
+// loads that allocate in L1 165).
 struct NormTask {
     const void* g;
     int64_t numel;
@@ -541,11 +540,12 @@ struct NormTable {
 };
 constexpr int kNormVecs = 4;
 
-__device__ __forceinline__ double widen(uint32_t bits) {       // |x|, see above
-    const uint32_t a = bits & 0x7FFFFFFFu;
-    return a ? __hiloint2double((int)((a >> 3) + 0x38000000u), (int)(a << 29)) : 0.0;
+__device__ __forceinline__ uint4 norm_load(const void* p) {
+    uint4 v;
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
-
 template <typename GT, int MAXT>
 __global__ void __launch_bounds__(kAdamThreads) k_grad_norm(const __grid_constant__ NormTable<MAXT> P) {
     constexpr int kVec = 16 / sizeof(GT);
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kAdamThreads) k_grad_norm(const __grid_constan
         for (int k = 0; k < kNormVecs; ++k) {
             const int64_t e = e0 + k * 32 * kVec;
             if (e + kVec <= T.numel) {
-                x[k] = __ldg(reinterpret_cast<const uint4*>(g + e));
+                x[k] = norm_load(g + e);
             } else {
                 x[k] = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -605,11 +605,11 @@ __global__ void __launch_bounds__(kAdamThreads) k_grad_norm(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (sizeof(GT) == 2) {
-                    const double a = widen(w[i] << 16), b = widen(w[i] & 0xFFFF0000u);
+                    const double a = (double)__uint_as_float(w[i] << 16), b = (double)__uint_as_float(w[i] & 0xFFFF0000u);
                     acc[i] = fma(a, a, acc[i]);
                     acc[i] = fma(b, b, acc[i]);
                 } else {
-                    const double a = widen(w[i]);
+                    const double a = (double)__uint_as_float(w[i]);
                     acc[i] = fma(a, a, acc[i]);
                 }
             }
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kAdamThreads) k_grad_norm(const __grid_constan
     const bool bad = !(f < __int_as_float(0x7F800000));
     float scale = 1.0f;
     if (P.max_norm > 0.0 && norm > 0.0) scale = (float)fmin(1.0, P.max_norm / norm);
-    P.out[0] = f;
+    P.out[0] = bad ? __int_as_float(0x7F800000) : f;
     P.out[1] = bad ? __int_as_float(0x7FC00000) : scale;
     if (P.d_step && !bad) *P.d_step += 1;
 }
