@@ -154,10 +154,14 @@ class ClockSampler:
                 "device_by": self.matched}
 
 
+# what the captured kernels and their launches are compiled from
+CAPTURED_SOURCES = ("qf_api.cu", "qf_device.cuh", "qf_lora.cuh", "qf_oneshot.cuh")
+
+
 def csrc_digest() -> str:
     h = hashlib.sha256()
     d = os.path.join(ROOT, "fp4_fake_quant_b200", "csrc")
-    for f in sorted(os.listdir(d)):
+    for f in CAPTURED_SOURCES:
         h.update(open(os.path.join(d, f), "rb").read())
     return h.hexdigest()[:16]
 

@@ -3,10 +3,20 @@
 // gx += s v A, gA = s v^T x, gB = s gy^T u), each token with the adapter of its request.
 //
 // Bound: HBM.  A rank-r product does r operations per byte of x (2 r per 2-byte element),
-// where the tensor cores' balance is 247: x, y, gy and gx are streamed once per kernel and
-// the factors, a few hundred KB, come from L2.  So the products run on mma.sync straight
-// from registers: with the reduction index permuted alike on both operands, the 16 bytes
-// a lane loads ARE its fragments, and no tile is staged through shared memory.
+// where the tensor cores' balance is 247: x, y, gy and gx are streamed once per kernel, the
+// factors, a few hundred KB, come from L2, and small batches are bound by launches and
+// waits.  The two reductions (down, and the factors' gradients) run on tcgen05: their
+// operands never pass through registers, which on mma.sync (512 multiply-adds a cycle and
+// SM) bound them at ranks from 32 up.  The product that adds to y keeps mma.sync (see up).
+//
+// Measured on a B200, back to back (floor: each operand once at 6.55 TB/s):
+//   forward 8192 x 4096 -> 14336, rank 16          92 us (82)
+//   its backward pass                             117 us (67; gy is read twice: 103)
+//   forward 16381 x 4096 -> 4096, ranks 8 to 64     98 us (52; 85 % of the tokens have one)
+//   its backward pass                             162 us (70; with gy twice 87)
+//   forward 8191 tokens of 37 requests, 14336 -> 4096, ranks 16 and 32   75 us (49)
+//   64 requests decoding, 24 adapters of ranks 8 to 64, 4096 -> 14336    18 us (4)
+//   1 token, 4096 -> 4096, rank 16                   5 us
 #pragma once
 
 #include <cstdint>
@@ -319,10 +329,10 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
 
 // One CTA's product in TMEM.  Warp 0 brings boxes of neighbouring rows by TMA, warp 1's
 // first lane issues the MMAs, warps 2 and 3 copy what is not a box by cp.async; all four
-// read the result.  (TMA's tile::gather4 for rows that are not neighbours took about 57
-// cycles a gather, 1800 for a step of 128 rows against 250 of cp.async: 8191 tokens of 37
-// requests x 14336 took 77 us with it.)  `full` of a stage: warp 0's expected bytes and the
-// copiers' arrivals; `empty`: its MMAs have committed.
+// read the result.  (TMA gathers of four rows instead of the copies took as long, 99 us for
+// the forward pass of 8191 tokens of 37 requests either way, and a second map per operand.)
+// `full` of a stage: warp 0's expected bytes and the copiers' arrivals; `empty`: its MMAs
+// have committed.
 constexpr int kTcThreads = 128, kCopiers = 64;
 template <int ST>
 struct TcPipe {
@@ -420,7 +430,9 @@ struct TcPipe {
 // depth; the CTAs of a cluster share one tile's steps and add their sums through
 // distributed shared memory in rank order, so the result does not depend on timing.
 // Rows behind the tile's last are not loaded, or are others': what lies there only reaches
-// its own results.
+// its own results.  235 MB (8192 x 14336, rank 16): 48 us, 4.9 TB/s, bound by the tail of a
+// wave whose CTAs differ and by the copies of F, which wait for L2 under load; 67 MB: 23 us,
+// of which about 9 are the start, the sums and the end.
 #ifndef QF_DOWN_STAGES
 #define QF_DOWN_STAGES 4
 #endif
@@ -536,7 +548,8 @@ k_lora_down(const __grid_constant__ AdapterTable<MAXA> A, const PlanView P, cons
 // stride ldy), read, added to in FP32 and rounded once.  Twice the bytes of the reductions
 // above for half the products: mma.sync keeps up here, and its accumulators lie in the
 // registers of the lanes that own y (tcgen05 with y tiles through shared memory and TMEM
-// took 95 us where this form takes 75).  A warp owns 32 columns of the tile's tokens and
+// took 95 us for 8192 x 14336 at rank 16 where this form takes 76; 63 for 16381 x 4096 at
+// ranks up to 64, where reading u from shared memory for each warp takes most).  A warp owns 32 columns of the tile's tokens and
 // keeps their factor rows as fragments; the columns are dealt to the four 8-wide MMA tiles
 // so that a lane ends up with 8 neighbouring columns of its rows: y moves in 16-byte
 // vectors, 64 bytes per row, four groups of 16 tokens ahead (cp.async, each lane exactly
@@ -899,7 +912,9 @@ k_lora_turn(const __grid_constant__ TurnTable<MAXA> A, int rows, int cols) {
 // gy.  The columns are the MMA's M, the high and low parts of v or u side by side its N, 64
 // gathered tokens a step its K; both operands lie in shared memory as in HBM, tokens
 // outermost, which the tensor core reads turned.  The CTAs of a cluster take slices of the
-// tokens and add up through distributed shared memory in rank order.
+// tokens and add up through distributed shared memory in rank order.  8192 tokens, 4096 and
+// 14336 columns, rank 16 (303 MB): 51 us, 5.9 TB/s; 13.9K tokens of 8 adapters, twice 4096
+// columns (232 MB from HBM, as much again of v and u from L2): 71 us.
 struct GradOut {
     void* ga;
     void* gb;

@@ -35,10 +35,13 @@
  *   - Arguments are validated on the host before anything is launched; an
  *     invalid call returns an error status and launches nothing.  A CUDA launch
  *     failure returns QF_ERR_CUDA.  Kernels never trap.  The one wait on other
- *     threads in the library is the grid barrier of qf_amax_fakequant's
- *     single-launch path, which is bounded (see there).  The LoRA kernels also
+ *     CTAs of a grid is the grid barrier of qf_amax_fakequant's single-launch path,
+ *     which is bounded (see there).  The LoRA kernels also
  *     wait, in hardware (cp.async.wait_group), for their own asynchronous copies
- *     of W into shared memory.
+ *     of W into shared memory.  The kernels of qf_lora_apply and its backward pass
+ *     wait on barriers in their own shared memory for their own copies and matrix
+ *     products, a bounded number of times (a CTA that gives up writes NaN), and, in
+ *     hardware (barrier.cluster), for the CTAs of their cluster.
  *     qf_last_error() gives a one-line description of the last failure on the
  *     calling thread.
  *   - Outputs must not overlap the inputs or one another, except that
@@ -48,7 +51,10 @@
  *   - Calls on the same stream are ordered; calls whose outputs overlap and that
  *     run concurrently on different streams race.
  *   - Numerics are fixed bit for bit (see each call); every result is
- *     deterministic and independent of launch configuration.
+ *     deterministic and independent of launch configuration.  qf_grad_norm,
+ *     qf_lora_apply and qf_lora_apply_backward document their own: their sums have an
+ *     order that is fixed for a device and the call's sizes, so equal calls give equal
+ *     bits.
  */
 #ifndef QF_H
 #define QF_H
@@ -431,7 +437,7 @@ typedef struct qf_param {
  *                  gradients were all zero becomes NaN)
  *   step           number of this step, from 1
  *   d_lr           NULL, or DEVICE FP32[1] that replaces lr
- *   d_step         NULL, or DEVICE int64[1] that replaces step
+ *   d_step         NULL, or DEVICE int64[1] (>= 1 when the call runs) that replaces step
  *   d_grad_scale   NULL, or DEVICE FP32[1] every gradient is multiplied with
  *                  (qf_grad_norm's d_norm + 1).  NaN: the step is skipped, every tensor
  *                  stays as it was.
@@ -509,8 +515,10 @@ size_t qf_grad_norm_workspace_bytes(void);
  * a 16-byte aligned; rank 1 .. QF_LORA_APPLY_MAX_RANK, the adapters' ranks may differ):
  *   u[t] = sum over c of x[t,c] a[k,c],  k < rank, kept as the sum of two BF16 values
  *   y[t] = BF16( y[t] + scale * sum over k of u[t,k] b[r,k] ),  r < rows
- * Sums in FP32 on the tensor cores, in an order that is fixed for a device, so equal calls
- * give equal bits.  A token without an adapter is left as it was (y, u, gx).
+ * Sums in FP32 on the tensor cores, in an order that is fixed for a device and the batch's
+ * sizes and grouping, so equal calls give equal bits.  A token without an adapter is left as
+ * it was (y, u, gx).  A NaN or an infinity in a token's x or gy reaches that token's rows and
+ * its adapter's gradients, nothing else.
  */
 #define QF_LORA_APPLY_MAX_RANK 128
 #define QF_LORA_MAX_ADAPTERS 512
