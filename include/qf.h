@@ -519,6 +519,8 @@ size_t qf_grad_norm_workspace_bytes(void);
  * sizes and grouping, so equal calls give equal bits.  A token without an adapter is left as
  * it was (y, u, gx).  A NaN or an infinity in a token's x or gy reaches that token's rows and
  * its adapter's gradients, nothing else.
+ * An infinity in b reaches its column of y, one in a its column of gx,
+ * as an infinity or, since u and v are sums of two values whose signs may differ, as a NaN.
  */
 #define QF_LORA_APPLY_MAX_RANK 128
 #define QF_LORA_MAX_ADAPTERS 512

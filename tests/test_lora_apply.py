@@ -345,6 +345,29 @@ def test_a_bad_token_stays_alone():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [20, 2000])                    # one launch, and two
+@pytest.mark.parametrize("rank", [8, 16, 24, 48, 80])             # with and without positions behind the rank
+def test_an_infinite_factor_stays_in_its_column(tokens, rank):
+    """An infinity in b[5, 0] (and in a[0, 7] backward) leaves y's column 5 (gx's column 7)
+    without a finite value, and every other bit as it is without it."""
+    cols, rows = 256, 512
+    clean, c = (Batch(torch.zeros(tokens), cols, rows, [rank], seed=3, plan=False) for _ in range(2))
+    keep = clean.dad[0][0][5, 0].clone()
+    c.dad[0][0][5, 0] = float("inf")
+    clean.forward()
+    c.forward()
+    torch.cuda.synchronize()
+    c.dad[0][0][5, 0], c.dad[0][1][0, 7] = keep, float("inf")
+    clean.backward(ga=None, gb=None)
+    c.backward(ga=None, gb=None)
+    torch.cuda.synchronize()
+    for name, at in (("y", 5), ("gx", 7)):
+        rest = torch.arange(c.dev[name].shape[1], device=DEV) != at
+        assert not c.dev[name][:, at].isfinite().any()
+        assert torch.equal(c.dev[name][:, rest], clean.dev[name][:, rest])
+
+
+@pytest.mark.gpu
 def test_the_plan_of_another_batch_changes_nothing():
     c = Batch(spread(100, 2, seed=8), 64, 64, [16, 8], seed=8)
     c.plan = torch.zeros_like(c.plan)
