@@ -8,6 +8,7 @@ libqf.so is missing or fails to load, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -163,6 +164,16 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _allocating_on(stream):
+    """Temporaries of a call belong to its stream: the allocator hands freed memory to later
+    work of the stream it was allocated on, which runs behind the call there and nowhere else."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 def _desc(xs: Sequence[torch.Tensor], ys=None, codes=None, scales=None, groups=None):
@@ -568,7 +579,9 @@ def qf_grad_norm(grads, norm, max_norm=0.0, step_tensor=None, workspace=None, st
     scale is NaN, which makes qf_adamw skip its step, when a gradient is not finite.
     ``step_tensor`` (int64) is advanced by one otherwise.  Without a ``workspace`` one is
     allocated for the call."""
-    prepare_grad_norm(grads, norm, max_norm, step_tensor, workspace)(stream)
+    with _allocating_on(stream):
+        call = prepare_grad_norm(grads, norm, max_norm, step_tensor, workspace)
+    call(stream)
     return norm
 
 
@@ -637,7 +650,8 @@ def qf_lora_plan(index: torch.Tensor, n_adapters: int, plan: Optional[torch.Tens
     """Group a batch's tokens by adapter: ``index`` int32, one entry per token (negative: no
     adapter).  One plan serves every projection of the batch."""
     if plan is None:
-        plan = alloc_lora_plan(index.numel(), n_adapters, index.device)
+        with _allocating_on(stream):
+            plan = alloc_lora_plan(index.numel(), n_adapters, index.device)
     prepare_lora_plan(index, n_adapters, plan)(stream)
     return plan
 
@@ -677,7 +691,8 @@ def qf_lora_apply(x, adapters, y, u=None, plan=None, stream=None) -> torch.Tenso
     qf_lora_plan, None: one adapter for every token).  ``y`` holds the shared projection's
     output.  Returns u = x a^T, which the backward call reads."""
     if u is None:
-        u = alloc_lora_u(x.numel() // max(x.shape[-1], 1), adapters)
+        with _allocating_on(stream):
+            u = alloc_lora_u(x.numel() // max(x.shape[-1], 1), adapters)
     prepare_lora_apply(x, adapters, y, u, plan)(stream)
     return u
 
@@ -713,4 +728,6 @@ def qf_lora_apply_backward(x, gy, adapters, u, gx=None, ga=None, gb=None, plan=N
     """gx += scale * (gy b) a; ga[i], gb[i] <- the gradients of adapter i's factors (zero
     without tokens).  ``gx`` holds the shared projection's own input gradient.  ``gx`` or
     the pair ``ga``/``gb`` may be left out."""
-    prepare_lora_apply_backward(x, gy, adapters, u, gx, ga, gb, plan, workspace)(stream)
+    with _allocating_on(stream):
+        call = prepare_lora_apply_backward(x, gy, adapters, u, gx, ga, gb, plan, workspace)
+    call(stream)

@@ -116,3 +116,39 @@ def test_the_steps_amax_feeds_the_next_forward_pass(bits):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o, w))
     assert step.item() == 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_temporaries_belong_to_the_calls_stream(raw, monkeypatch):
+    """What a call allocates for itself comes from the stream it runs on, whichever is current."""
+    gen = torch.Generator().manual_seed(2)
+    x, gy = _randn(gen, 40, 64), _randn(gen, 40, 32)
+    adapters = [(_randn(gen, 32, 8), _randn(gen, 8, 64), 1.0)]
+    index, norm = torch.zeros(40, dtype=torch.int32, device=DEV), torch.empty(2, device=DEV)
+    y, gx = torch.zeros_like(gy), torch.zeros_like(x)
+    ga, gb = [torch.empty_like(adapters[0][1])], [torch.empty_like(adapters[0][0])]
+    seen = []
+
+    def noting(name):
+        alloc = getattr(qf.binding, name)
+
+        def noted(*args):
+            seen.append((name, torch.cuda.current_stream().cuda_stream))
+            return alloc(*args)
+        monkeypatch.setattr(qf.binding, name, noted)
+    names = ["alloc_lora_plan", "alloc_lora_u", "alloc_lora_workspace", "alloc_grad_norm_workspace"]
+    for name in names:
+        noting(name)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    plan = qf.qf_lora_plan(index, 1, stream=stream)
+    u = qf.qf_lora_apply(x, adapters, y, plan=plan, stream=stream)
+    qf.qf_lora_apply_backward(x, gy, adapters, u, gx, ga, gb, plan=plan, stream=stream)
+    qf.qf_grad_norm(ga + gb, norm, stream=stream)
+    assert seen == [(name, side.cuda_stream) for name in names]
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    side.synchronize()
+    total = sum(float(g.double().square().sum()) for g in ga + gb) ** 0.5
+    assert total > 0 and abs(norm[0].item() - total) <= total * 2.0 ** -23
